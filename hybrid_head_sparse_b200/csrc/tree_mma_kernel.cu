@@ -1,0 +1,755 @@
+// tree_mma_kernel.cu -- attention of a few query rows over the cache
+// (lyc_tree_attention), bf16 or e4m3 rows, on mma.sync.
+//
+// For every element, KV head and block of up to 16 or 32 of its G * T query
+// rows (row i = node i / G, head g * G + i % G):
+//   z[i][j] = scale log2(e) q_i . k_j  (-inf where node i does not see row j)
+//   o_i = sum_j 2^(z[i][j] - m_i) v_j / sum_j 2^(z[i][j] - m_i)
+// in one pass with a running maximum m and sum per row.
+//
+// With few query rows a call reads every cached byte once and does 4 G T flop
+// for each element of K: HBM bounds it, and what counts is bytes in flight.
+// Eight warps a CTA, one CTA an SM; each warp takes its own 4 KiB of K and of
+// V rows out of every tile through a ring of stages that only it uses, filled
+// with 16-byte cp.async, so no warp waits for another until the end of the
+// CTA's run of tiles, where the eight states are merged in shared memory.
+//
+// 8-bit rows: codes become f16 by moving bits (value * 2^-8, exact), so both
+// products run in f16 with fp32 sums.  Which elements share a register is
+// free in a sum over the head's dimensions, so K's codes are read 16 bytes at
+// a time in an order that needs no shuffling and Q is laid out to match.  A
+// query row is scaled by a power of two to below 2 before it becomes f16
+// (exact for elements down to 2^-14 of the row's largest).  V's scales 2^e_j
+// go into the exponent: p'_j = 2^(z_j + e_j - m'), m' the running maximum of
+// z_j + e_j, so p' stays in f16's range whatever the scales are, and the sum
+// takes p'_j 2^-e_j.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "lyc_device.cuh"
+#include "serve_plan.h"
+#include "tree_sched.cuh"
+
+namespace lyc {
+
+namespace {
+
+template <int D_, bool F8_, int MT_>
+struct TmCfg {
+  static constexpr int D = D_;
+  static constexpr bool F8 = F8_;
+  static constexpr int MT = MT_;                // 16-row blocks of queries
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int NW = 8;
+  static constexpr int THREADS = NW * 32;
+  static constexpr int ROWB = D * (F8 ? 1 : 2);
+  static constexpr int KC = 4096 / ROWB;        // rows of a warp's chunk
+  static constexpr int TR = NW * KC;            // rows of a tile
+  static constexpr int LPR = ROWB / 16;         // 16-byte pieces of a row
+  static constexpr int RPI = 32 / LPR;          // rows of one warp-wide copy
+  static constexpr int KPL = (KC + 31) / 32;    // rows a lane looks up
+  static constexpr int ST = 3;                  // stages
+  static constexpr int WARPB = ST * 8192;       // a warp's ring
+  static constexpr int OFF_SC = NW * WARPB;     // per warp and stage: K factor, V exponent, 2^-exponent
+  static constexpr int SCB = F8 ? KC * 12 : 0;
+  static constexpr int OFF_OK = OFF_SC + NW * ST * SCB;  // per warp and stage: rows that exist
+  static constexpr int OFF_ML = OFF_OK + NW * ST * 8;    // per warp and row: (m, l)
+  static constexpr int SMEM = OFF_ML + NW * ROWS * 8;
+  static_assert(ROWS * D * 4 <= WARPB, "a warp's output fits its ring");
+};
+
+// byte offset of 16-byte piece ch of row r in a chunk
+template <class C>
+__device__ __forceinline__ int k_off(int r, int ch) {
+  if (!C::F8) return (ch >> 3) * (C::KC * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  if (C::D == 128) return r * 128 + ((ch ^ ((r & 1) << 2)) << 4);
+  return r * 64 + (ch << 4);
+}
+template <class C>
+__device__ __forceinline__ int v_off(int r, int ch) {
+  if (!C::F8) return (ch >> 3) * (C::KC * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  if (C::D == 128) return r * 128 + ((ch ^ (r & 7)) << 4);
+  return (r >> 1) * 128 + ((((r & 1) << 2) + (ch ^ ((r >> 1) & 3))) << 4);
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F8>
+__device__ __forceinline__ void mma16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (F8)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <bool F8>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (F8)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// e4m3 codes in bytes 1 and 3 (0 and 2) as f16 of value * 2^-8: the sign stays,
+// the four exponent and three mantissa bits move to the low end of f16's
+// exponent and the top of its mantissa.
+__device__ __forceinline__ uint32_t codes13(uint32_t w) { return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u); }
+__device__ __forceinline__ uint32_t codes02(uint32_t w) { return codes13(w << 8); }
+
+__device__ __forceinline__ uint16_t bf16_bits(const unsigned char* p) { return *reinterpret_cast<const uint16_t*>(p); }
+
+// A piece of work: tiles [t0, t1) of group (b, g, mb).
+struct TmPiece {
+  int b, g, mb, t0, t1;
+  TreeElem e;
+};
+
+// The loads of one warp's chunks: where each row lies is looked up one chunk
+// ahead of its copies, its scale bytes are kept in registers for one chunk
+// before they go to shared memory.
+template <class C>
+struct TmLoader {
+  const TreeParams& p;
+  const TmPiece& pc;
+  unsigned char* ring;
+  float* scales;
+  unsigned long long* okw;
+  int warp, lane, nchunks;
+  RowAt at[C::KPL];
+  unsigned long long ok;  // rows of the looked-up chunk that exist
+  int kb[C::KPL], vb[C::KPL];  // scale bytes waiting for shared memory
+  int pending;                 // their stage, or -1
+
+  __device__ __forceinline__ TmLoader(const TreeParams& prm, const TmPiece& piece, unsigned char* smem, int w, int l)
+      : p(prm), pc(piece), ring(smem + w * C::WARPB),
+        scales(reinterpret_cast<float*>(smem + C::OFF_SC + w * C::ST * C::SCB)),
+        okw(reinterpret_cast<unsigned long long*>(smem + C::OFF_OK) + w * C::ST), warp(w), lane(l),
+        nchunks(piece.t1 - piece.t0), pending(-1) {}
+
+  __device__ __forceinline__ int first_row(int i) const { return (pc.t0 + i) * C::TR + warp * C::KC; }
+
+  __device__ __forceinline__ void look_up(int i) {
+    ok = 0;
+    if (i >= nchunks) return;
+    const int base = first_row(i);
+#pragma unroll
+    for (int k = 0; k < C::KPL; ++k) {
+      const int r = k * 32 + lane;
+      const bool in = r < C::KC && base + r < pc.e.n;
+      bool found = false;
+      at[k] = RowAt{0, 0};
+      if (in) {
+        found = cache_row(p.cache, pc.b, base + r, &at[k]);
+        if (!found) at[k] = RowAt{0, 0};
+      }
+      if (in && !found && p.status) atomicOr(p.status, LYC_OP_BAD_PAGE);
+      const unsigned long long m = __ballot_sync(0xffffffffu, found);
+      ok |= m << (32 * k);
+    }
+  }
+  __device__ __forceinline__ void flush_scales() {
+    if (!C::F8 || pending < 0) return;
+    float* s = scales + pending * (C::KC * 3);
+#pragma unroll
+    for (int k = 0; k < C::KPL; ++k) {
+      const int r = k * 32 + lane;
+      if (r < C::KC) {
+        const float nan = __uint_as_float(0x7fffffffu);
+        s[r] = kb[k] == 255 ? nan : __uint_as_float(static_cast<uint32_t>(kb[k]) << 23);
+        s[C::KC + r] = vb[k] == 255 ? nan : static_cast<float>(vb[k] - 127);
+        // finite for a NaN row too: its exponent makes p NaN where it is seen, and 0 * NaN is not 0 where not
+        s[2 * C::KC + r] = vb[k] == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(254 - vb[k], 1)) << 23);
+      }
+    }
+    pending = -1;
+  }
+  // copies of chunk i (looked up before) into its stage
+  __device__ __forceinline__ void issue(int i) {
+    if (i < nchunks) {
+      const int stage = i % C::ST;
+      unsigned char* k = ring + stage * 8192;
+      const int ch = lane % C::LPR;
+      const unsigned char* kg = p.cache.k + pc.g * p.cache.s_head * (C::F8 ? 1 : 2) + ch * 16;
+      const unsigned char* vg = p.cache.v + pc.g * p.cache.s_head * (C::F8 ? 1 : 2) + ch * 16;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int r = s * C::RPI + lane / C::LPR;
+        const int64_t kv = __shfl_sync(0xffffffffu, at[(s * C::RPI) / 32].kv, r & 31);
+        const bool have = (ok >> r) & 1ull;
+        const int64_t off = have ? kv * (C::F8 ? 1 : 2) : 0;
+        cp16(smem_u32(k + k_off<C>(r, ch)), kg + off, have ? 16 : 0);
+        cp16(smem_u32(k + 4096 + v_off<C>(r, ch)), vg + off, have ? 16 : 0);
+      }
+      if (lane == 0) okw[stage] = ok;
+      if (C::F8) {
+#pragma unroll
+        for (int j = 0; j < C::KPL; ++j) {
+          const int r = j * 32 + lane;
+          kb[j] = vb[j] = 127;
+          if (r < C::KC && ((ok >> r) & 1ull)) {
+            kb[j] = p.cache.ks[at[j].sc + pc.g * p.cache.ss_head];
+            vb[j] = p.cache.vs[at[j].sc + pc.g * p.cache.ss_head];
+          }
+        }
+        pending = stage;
+      }
+    }
+    cp_commit();
+  }
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int D = C::D, MT = C::MT, KS = D / 16, NT = D / 8;
+  constexpr unsigned FULL = 0xffffffffu;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g4 = lane >> 2, j4 = lane & 3;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (blockIdx.x == 0 && p.status)
+    for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
+      bool bad = false;
+      tree_elem(p, b, &bad);
+      if (bad) atomicOr(p.status, LYC_OP_BAD_LENGTH);
+    }
+  const TreeSched<C::TR> sched(p);
+  const int cta = blockIdx.x;
+  const int64_t xbeg = sched.begin(cta), xend = sched.begin(cta + 1);
+  const float NEG = -INFINITY;
+
+  for (int64_t x = xbeg; x < xend;) {
+    TmPiece pc;
+    int64_t efirst;
+    sched.locate(x, &pc.b, &efirst);
+    bool bad = false;
+    pc.e = tree_elem(p, pc.b, &bad);
+    const int nt = (pc.e.n + C::TR - 1) / C::TR;
+    const int64_t rel = x - efirst;
+    const int grp = static_cast<int>(rel / nt);
+    pc.g = grp / p.mblocks;
+    pc.mb = grp % p.mblocks;
+    pc.t0 = static_cast<int>(rel - static_cast<int64_t>(grp) * nt);
+    pc.t1 = static_cast<int>(min(static_cast<int64_t>(nt), pc.t0 + (xend - x)));
+    x += pc.t1 - pc.t0;
+
+    const int first_draft = pc.e.n - pc.e.cnt;
+    TmLoader<C> ld(p, pc, smem, warp, lane);
+    ld.look_up(0);
+#pragma unroll
+    for (int i = 0; i < C::ST - 1; ++i) {
+      ld.flush_scales();
+      ld.issue(i);
+      ld.look_up(i + 1);
+    }
+
+    // the queries: rows g4 and g4 + 8 of each 16-row block
+    uint32_t qa[MT][KS][4];
+    float rowf[MT][2];  // logits factor of the row (F8: with the row's power of two)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int i = pc.mb * C::ROWS + mt * 16 + hf * 8 + g4;
+        const int t = i / p.G, h = pc.g * p.G + i % p.G;
+        const bool live = t < pc.e.cnt;
+        const unsigned char* src = p.q + 2 * (pc.b * p.q_batch + t * p.q_token + h * p.q_head);
+        rowf[mt][hf] = p.scale_log2;
+        if (!C::F8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qa[mt][ks][hf + 2 * e] =
+                  live ? *reinterpret_cast<const uint32_t*>(src + 2 * (ks * 16 + e * 8 + j4 * 2)) : 0u;
+        } else {
+          // dims 64 blk + 16 j4 + 4 s + {0, 2} and {1, 3} of step 4 blk + s
+          uint32_t raw[D / 64][8];
+          uint32_t mx = 0;
+#pragma unroll
+          for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              uint4 u = make_uint4(0u, 0u, 0u, 0u);
+              if (live) u = *reinterpret_cast<const uint4*>(src + 2 * (blk * 64 + j4 * 16 + v * 8));
+              raw[blk][4 * v] = u.x;
+              raw[blk][4 * v + 1] = u.y;
+              raw[blk][4 * v + 2] = u.z;
+              raw[blk][4 * v + 3] = u.w;
+            }
+#pragma unroll
+          for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mx = max(mx, max(raw[blk][k] & 0x7fffu, (raw[blk][k] >> 16) & 0x7fffu));
+          mx = max(mx, __shfl_xor_sync(FULL, mx, 1));
+          mx = max(mx, __shfl_xor_sync(FULL, mx, 2));
+          int ex = static_cast<int>(mx >> 7);  // biased exponent of the row's largest element
+          if (ex == 0 || ex == 255) ex = 127;
+          // the power of two comes off in two factors: 2^-(ex - 127) may be out of fp32's range
+          const int e1 = (ex - 127) / 2, e2 = ex - 127 - e1;
+          const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+          const float f2 = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+          // K's codes are read as value * 2^-8
+          rowf[mt][hf] = p.scale_log2 * 256.f * __uint_as_float(static_cast<uint32_t>(ex) << 23);
+#pragma unroll
+          for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+              const uint32_t w0 = raw[blk][2 * s], w1 = raw[blk][2 * s + 1];
+              qa[mt][blk * 4 + s][hf] = pack16<true>(bf16lo(w0) * f1 * f2, bf16lo(w1) * f1 * f2);
+              qa[mt][blk * 4 + s][hf + 2] = pack16<true>(bf16hi(w0) * f1 * f2, bf16hi(w1) * f1 * f2);
+            }
+        }
+      }
+
+    float o[MT][NT][4];
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[mt][n][c] = 0.f;
+      m[mt][0] = m[mt][1] = NEG;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+
+    for (int i = 0; i < ld.nchunks; ++i) {
+      ld.flush_scales();
+      cp_wait<C::ST - 2>();
+      __syncwarp();
+      ld.issue(i + C::ST - 1);
+      ld.look_up(i + C::ST);
+      const int base = ld.first_row(i);
+      if (base >= pc.e.n) continue;
+      const int stage = i % C::ST;
+      unsigned char* kbuf = ld.ring + stage * 8192;
+      unsigned char* vbuf = kbuf + 4096;
+      const unsigned long long ok = ld.okw[stage];
+      const float* sc = ld.scales + stage * (C::KC * 3);
+
+#pragma unroll 1
+      for (int sub = 0; sub < C::KC / 16; ++sub) {
+        const int key0 = base + sub * 16;
+        if (key0 >= pc.e.n) break;
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[mt][t][c] = 0.f;
+        if (!C::F8) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            uint32_t kf[4];
+            ldsm4(kf, smem_u32(kbuf + k_off<C>(sub * 16 + ((lane >> 4) << 3) + (lane & 7), ks * 2 + ((lane >> 3) & 1))));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16<false>(s[mt][0], qa[mt][ks], kf[0], kf[1]);
+              mma16<false>(s[mt][1], qa[mt][ks], kf[2], kf[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int blk = 0; blk < D / 64; ++blk) {
+              const uint4 u = *reinterpret_cast<const uint4*>(kbuf + k_off<C>(sub * 16 + t * 8 + g4, blk * 4 + j4));
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+              for (int st = 0; st < 4; ++st) {
+                const uint32_t b0 = codes02(w[st]), b1 = codes13(w[st]);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma16<true>(s[mt][t], qa[mt][blk * 4 + st], b0, b1);
+              }
+            }
+        }
+        // log2-unit logits, with V's exponent where rows are scaled
+        float isv[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (C::F8) {
+            const int k = sub * 16 + t * 8 + 2 * j4;
+            const float2 kf = *reinterpret_cast<const float2*>(sc + k);
+            const float2 ev = *reinterpret_cast<const float2*>(sc + C::KC + k);
+            const float2 iv = *reinterpret_cast<const float2*>(sc + 2 * C::KC + k);
+            isv[t][0] = iv.x;
+            isv[t][1] = iv.y;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                s[mt][t][c] = fmaf(s[mt][t][c] * rowf[mt][c >> 1], (c & 1) ? kf.y : kf.x, (c & 1) ? ev.y : ev.x);
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) s[mt][t][c] *= rowf[mt][c >> 1];
+          }
+        }
+        const uint32_t okh = static_cast<uint32_t>(ok >> (sub * 16)) & 0xffffu;
+        const bool masked = okh != 0xffffu || key0 + 16 > first_draft;
+        if (masked) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int t = (pc.mb * C::ROWS + mt * 16 + (c >> 1) * 8 + g4) / p.G;
+#pragma unroll
+              for (int tl = 0; tl < 2; ++tl) {
+                const int kk = tl * 8 + 2 * j4 + (c & 1);
+                const int node = key0 + kk - first_draft;
+                const bool sees = ((okh >> kk) & 1u) &&
+                                  (node < 0 || (t < pc.e.cnt && node < pc.e.cnt && tree_sees(p, pc.b, t, node)));
+                if (!sees) s[mt][tl][c] = NEG;
+              }
+            }
+        }
+        // the running maxima move only when some row's grows by more than 2^8
+        bool grow = false;
+        float mx[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            mx[mt][hf] = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]), fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+            grow |= mx[mt][hf] > m[mt][hf] + 8.f;
+          }
+        if (__any_sync(FULL, grow)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float r = mx[mt][hf];
+              r = fmaxf(r, __shfl_xor_sync(FULL, r, 1));
+              r = fmaxf(r, __shfl_xor_sync(FULL, r, 2));
+              if (r > m[mt][hf] + 8.f) {
+                const float f = m[mt][hf] == NEG ? 1.f : ex2(m[mt][hf] - r);  // 1: the state is zero, or NaN
+                m[mt][hf] = r;
+                l[mt][hf] *= f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  o[mt][n][2 * hf] *= f;
+                  o[mt][n][2 * hf + 1] *= f;
+                }
+              }
+            }
+        }
+        uint32_t pa[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            // f16's range is used from the top: p' up to 2^(8 + 6)
+            const float neg = (m[mt][hf] == NEG ? 0.f : -m[mt][hf]) + (C::F8 ? 6.f : 0.f);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const float p0 = ex2(s[mt][t][2 * hf] + neg), p1 = ex2(s[mt][t][2 * hf + 1] + neg);
+              if (C::F8)
+                l[mt][hf] = fmaf(p0, isv[t][0], fmaf(p1, isv[t][1], l[mt][hf]));
+              else
+                l[mt][hf] += p0 + p1;
+              pa[mt][hf + 2 * t] = pack16<C::F8>(p0, p1);
+            }
+          }
+        if (!C::F8 && key0 + 16 > first_draft) {
+          // drafted rows that some queries do not see: a NaN or an infinity in V
+          // would reach every row through the product (0 * NaN), so it is added
+          // to the rows that see it and taken out of the tile
+          bool odd = false;
+          for (int e = lane; e < 16 * (D / 8); e += 32) {
+            const int r = e / (D / 8), ch = e % (D / 8);
+            const uint4 u = *reinterpret_cast<const uint4*>(vbuf + v_off<C>(sub * 16 + r, ch));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              odd |= (w[k] & 0x7f80u) == 0x7f80u || (w[k] & 0x7f800000u) == 0x7f800000u;
+          }
+          if (__any_sync(FULL, odd)) {
+            for (int kk = 0; kk < 16; ++kk) {
+              const int node = key0 + kk - first_draft;
+              if (!((okh >> kk) & 1u)) continue;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                  const int t = (pc.mb * C::ROWS + mt * 16 + hf * 8 + g4) / p.G;
+                  const bool sees = node < 0 || (t < pc.e.cnt && node < pc.e.cnt && tree_sees(p, pc.b, t, node));
+                  if (!sees) continue;
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                      const uint32_t v = bf16_bits(vbuf + v_off<C>(sub * 16 + kk, n) + (2 * j4 + c) * 2);
+                      if ((v & 0x7f80u) == 0x7f80u) o[mt][n][2 * hf + c] += __uint_as_float(v << 16);
+                    }
+                }
+            }
+            __syncwarp();
+            for (int e = lane; e < 16 * D; e += 32) {
+              unsigned char* q = vbuf + v_off<C>(sub * 16 + e / D, (e % D) / 8) + (e % 8) * 2;
+              if ((bf16_bits(q) & 0x7f80u) == 0x7f80u) *reinterpret_cast<uint16_t*>(q) = 0;
+            }
+            __syncwarp();
+          }
+        }
+        if (!C::F8) {
+#pragma unroll
+          for (int dt = 0; dt < D / 16; ++dt) {
+            uint32_t vf[4];
+            ldsm4t(vf, smem_u32(vbuf + v_off<C>(sub * 16 + (lane & 15), dt * 2 + (lane >> 4))));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16<false>(o[mt][2 * dt], pa[mt], vf[0], vf[1]);
+              mma16<false>(o[mt][2 * dt + 1], pa[mt], vf[2], vf[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int dt = 0; dt < D / 32; ++dt) {
+            uint32_t vf[4];
+            ldsm4t(vf, smem_u32(vbuf + v_off<C>(sub * 16 + (lane & 15), dt * 2 + (lane >> 4))));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t e0 = codes02(vf[2 * half]), e1 = codes02(vf[2 * half + 1]);
+              const uint32_t o0 = codes13(vf[2 * half]), o1 = codes13(vf[2 * half + 1]);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma16<true>(o[mt][4 * dt + 2 * half], pa[mt], e0, e1);
+                mma16<true>(o[mt][4 * dt + 2 * half + 1], pa[mt], o0, o1);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+    cp_wait<0>();
+
+    // merge the eight warps' states; each warp's output goes into its ring
+    float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+    float* ow = reinterpret_cast<float*>(ld.ring);
+    __syncwarp();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int row = mt * 16 + hf * 8 + g4;
+        float ls = l[mt][hf];
+        ls += __shfl_xor_sync(FULL, ls, 1);
+        ls += __shfl_xor_sync(FULL, ls, 2);
+        if (j4 == 0) ml[warp * C::ROWS + row] = make_float2(m[mt][hf], ls);
+        if (!C::F8) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<float2*>(ow + row * D + n * 8 + 2 * j4) =
+                make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+        } else {
+          // V's codes were read as value * 2^-8; tiles 2c and 2c + 1 hold the even and odd dims
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c)
+            *reinterpret_cast<float4*>(ow + row * D + c * 16 + 4 * j4) =
+                make_float4(o[mt][2 * c][2 * hf] * 256.f, o[mt][2 * c + 1][2 * hf] * 256.f,
+                            o[mt][2 * c][2 * hf + 1] * 256.f, o[mt][2 * c + 1][2 * hf + 1] * 256.f);
+        }
+      }
+    __syncthreads();
+    {
+      constexpr int TPR = C::THREADS / C::ROWS, DPT = D / TPR;
+      const int row = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * DPT;
+      float M = NEG, L = 0.f, acc[DPT];
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[w * C::ROWS + row].x);
+#pragma unroll
+      for (int k = 0; k < DPT; ++k) acc[k] = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::NW; ++w) {
+        const float2 s = ml[w * C::ROWS + row];
+        const float f = s.x == NEG ? 1.f : ex2(s.x - M);  // 1: the state is zero, or NaN
+        L = fmaf(s.y, f, L);
+        const float* src = reinterpret_cast<const float*>(smem + w * C::WARPB) + row * D + d0;
+#pragma unroll
+        for (int k = 0; k < DPT; ++k) acc[k] = fmaf(src[k], f, acc[k]);
+      }
+      const int i = pc.mb * C::ROWS + row;
+      const int t = i / p.G, h = pc.g * p.G + i % p.G;
+      if (t < pc.e.cnt) {
+        if (pc.t0 == 0 && pc.t1 == nt) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          unsigned char* dst = p.out + 2 * (pc.b * p.o_batch + t * p.o_token + h * p.o_head + d0);
+#pragma unroll
+          for (int k = 0; k < DPT; k += 2)
+            reinterpret_cast<uint32_t*>(dst)[k / 2] = pack16<false>(acc[k] * inv, acc[k + 1] * inv);
+        } else {
+          const int64_t slot = 2 * static_cast<int64_t>(cta) + (pc.t0 == 0 ? 1 : 0);
+          float* dst = p.part_o + (slot * C::ROWS + row) * D + d0;
+#pragma unroll
+          for (int k = 0; k < DPT; k += 4)
+            *reinterpret_cast<float4*>(dst + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
+          if (d0 == 0) p.part_ml[slot * C::ROWS + row] = make_float2(M, L);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// One warp for each query row of each group: merges the states of the CTAs
+// among which the group was cut, in their order.
+template <int D, int ROWS, int TR>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeParams p) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  const TreeSched<TR> sched(p);
+  if (sched.total == 0) return;
+  const int rows = p.G * p.T;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int i = static_cast<int>(w % rows);
+  const int64_t bg = w / rows;
+  const int g = static_cast<int>(bg % p.Hkv);
+  const int64_t b = bg / p.Hkv;
+  if (b >= p.B) return;
+  bool bad = false;
+  const TreeElem e = tree_elem(p, static_cast<int>(b), &bad);
+  const int t = i / p.G, h = g * p.G + i % p.G;
+  if (t >= e.cnt) return;
+  const int mb = i / ROWS, row = i % ROWS;
+  const int nt = (e.n + TR - 1) / TR;
+  const int64_t x0 = sched.first_tile(static_cast<int>(b)) + static_cast<int64_t>(g * p.mblocks + mb) * nt;
+  const int c0 = sched.owner(x0), c1 = sched.owner(x0 + nt - 1);
+  if (c0 == c1) return;  // its CTA wrote the output
+  constexpr int V = D / 32;
+  auto slot_of = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * ROWS + row; };
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[slot_of(c)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f, acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const int64_t s = slot_of(c);
+    const float2 ml = p.part_ml[s];
+    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);  // 1: the state is zero, or NaN
+    L = fmaf(ml.y, f, L);
+    const float* src = p.part_o + s * D + lane * V;
+    if (V == 4) {
+      const float4 u = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(u.x, f, acc[0]);
+      acc[1] = fmaf(u.y, f, acc[1]);
+      acc[V - 2] = fmaf(u.z, f, acc[V - 2]);
+      acc[V - 1] = fmaf(u.w, f, acc[V - 1]);
+    } else {
+      const float2 u = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(u.x, f, acc[0]);
+      acc[1] = fmaf(u.y, f, acc[1]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  unsigned char* dst = p.out + 2 * (b * p.o_batch + t * p.o_token + h * p.o_head + lane * V);
+#pragma unroll
+  for (int k = 0; k < V; k += 2)
+    reinterpret_cast<uint32_t*>(dst)[k / 2] = pack16<false>(acc[k] * inv, acc[k + 1] * inv);
+}
+
+template <class C>
+cudaError_t launch_mma(const TreeParams* p, int device, cudaStream_t stream) {
+  static std::atomic<bool> configured[64];  // per device; setting the attribute twice does no harm
+  if (device >= 64 || !configured[device].load(std::memory_order_relaxed)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(tree_mma_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (device < 64) configured[device].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p->grid));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_mma_kernel<C>, *p);
+}
+
+template <int D, int ROWS, int TR>
+cudaError_t launch_combine(const TreeParams* p, cudaStream_t stream) {
+  const int64_t warps = static_cast<int64_t>(p->B) * p->Hkv * p->G * p->T;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, ROWS, TR>, *p);
+}
+
+}  // namespace
+
+int tree_mma_tile_rows(int head_dim, int cache_type) {
+  return 8 * 4096 / (head_dim * (cache_type == LYC_CACHE_E4M3 ? 1 : 2));
+}
+
+int tree_mma_block_rows(int rows) { return rows <= 16 ? 16 : 32; }
+
+cudaError_t tree_mma_launch(const TreeParams* p, int head_dim, int cache_type, int block_rows, int device,
+                            cudaStream_t stream) {
+  const bool f8 = cache_type == LYC_CACHE_E4M3;
+#define LYC_TREE(DD, FF)                                                           \
+  (block_rows == 16 ? launch_mma<TmCfg<DD, FF, 1>>(p, device, stream)              \
+                    : launch_mma<TmCfg<DD, FF, 2>>(p, device, stream))
+  if (head_dim == 128) return f8 ? LYC_TREE(128, true) : LYC_TREE(128, false);
+  return f8 ? LYC_TREE(64, true) : LYC_TREE(64, false);
+#undef LYC_TREE
+}
+
+cudaError_t tree_combine_launch(const TreeParams* p, int head_dim, int block_rows, int tile_rows,
+                                cudaStream_t stream) {
+#define LYC_COMBINE(DD, TT) \
+  (block_rows == 16 ? launch_combine<DD, 16, TT>(p, stream) : launch_combine<DD, 32, TT>(p, stream))
+  if (head_dim == 128) return tile_rows == 128 ? LYC_COMBINE(128, 128) : LYC_COMBINE(128, 256);
+  return tile_rows == 256 ? LYC_COMBINE(64, 256) : LYC_COMBINE(64, 512);
+#undef LYC_COMBINE
+}
+
+}  // namespace lyc

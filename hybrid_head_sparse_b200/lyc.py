@@ -52,12 +52,20 @@ LYC_RULE_THRESHOLD = 4
 LYC_TOPK_FIXED = 0
 LYC_TOPK_RULES = 1
 
+LYC_CACHE_BF16 = 0
+LYC_CACHE_E4M3 = 1
+LYC_OP_BAD_LENGTH = 0x1
+LYC_OP_BAD_PAGE = 0x2
+LYC_OP_BAD_INDEX = 0x4
+
 EXPORTED = ["lyc_create", "lyc_decode_step", "lyc_decode_step_host", "lyc_decode_step_batch",
             "lyc_sync_status",
             "lyc_set_s_trace", "lyc_step_bytes", "lyc_step_launches", "lyc_topk_f32", "lyc_topk_f32_ex",
             "lyc_set_timing",
             "lyc_kernel_times", "lyc_set_timeline", "lyc_status_string", "lyc_last_error",
-            "lyc_destroy", "lyc_sparse_attention_noalloc", "lyc_set_selection", "lyc_cache_correction"]
+            "lyc_destroy", "lyc_sparse_attention_noalloc", "lyc_set_selection", "lyc_cache_correction",
+            "lyc_qk_norm_rope", "lyc_cache_append", "lyc_cache_read", "lyc_tree_workspace_bytes",
+            "lyc_tree_attention", "lyc_operator_error"]
 
 
 class lyc_config(ctypes.Structure):
@@ -93,6 +101,42 @@ class lyc_selection(ctypes.Structure):
 
 class lyc_kernel_time(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("layer", ctypes.c_int), ("ms", ctypes.c_float)]
+
+
+def _struct(name, doc, **fields):
+    """A ctypes mirror of a struct of include/lyc.h: p = pointer, i = int32, l = int64, f = float,
+    each value the fields of that type in a row, in the header's order."""
+    types = {"p": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64, "f": ctypes.c_float}
+    flat = [(n, types[key[0]]) for key, names in fields.items() for n in names.split()]
+    return type(name, (ctypes.Structure,), {"_fields_": flat, "__doc__": doc})
+
+
+lyc_layer_cache = _struct(
+    "lyc_layer_cache", "One layer's cache (include/lyc.h).",
+    p1="k v k_scale v_scale",
+    l1="s_batch s_head s_token s_page ss_batch ss_head ss_token ss_page",
+    p2="block_table", l2="rows num_pages",
+    i1="page_rows max_blocks type batch num_kv_heads head_dim device")
+lyc_rope_args = _struct(
+    "lyc_rope_args", "Arguments of lyc_qk_norm_rope.",
+    p1="q k q_out k_out",
+    l1="q_row q_head k_row k_head qo_row qo_head ko_row ko_head",
+    p2="pos inv_freq q_weight k_weight", l2="rows",
+    i1="num_q_heads num_kv_heads head_dim rot_dim interleaved", f1="eps", i2="dtype device")
+lyc_append_args = _struct(
+    "lyc_append_args", "Arguments of lyc_cache_append.",
+    p1="k v q q_out",
+    l1="k_batch k_token k_head v_batch v_token v_head q_batch q_token q_head qo_batch qo_token qo_head",
+    p2="n t_len pos inv_freq q_weight k_weight",
+    i1="T num_q_heads rot_dim interleaved", f1="eps", p3="status")
+lyc_read_args = _struct(
+    "lyc_read_args", "Arguments of lyc_cache_read.",
+    p1="k_out v_out", l1="o_batch o_head o_row", p2="n sets", l2="first",
+    i1="m num_heads dtype", p3="status")
+lyc_tree_args = _struct(
+    "lyc_tree_args", "Arguments of lyc_tree_attention.",
+    p1="q out", l1="q_batch q_token q_head o_batch o_token o_head",
+    p2="n t_len mask", i1="T num_q_heads", f1="scale", p3="workspace", l2="workspace_bytes", p4="status")
 
 
 class LycError(RuntimeError):
@@ -141,9 +185,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.lyc_destroy.restype = None
     L.lyc_sparse_attention_noalloc.argtypes = [P, ctypes.POINTER(lyc_kv_cache), I, I, I, I, P, I,
                                                P, P, P]
+    L.lyc_qk_norm_rope.argtypes = [ctypes.POINTER(lyc_rope_args), P]
+    L.lyc_cache_append.argtypes = [ctypes.POINTER(lyc_layer_cache), ctypes.POINTER(lyc_append_args), P]
+    L.lyc_cache_read.argtypes = [ctypes.POINTER(lyc_layer_cache), ctypes.POINTER(lyc_read_args), P]
+    L.lyc_tree_workspace_bytes.argtypes = [ctypes.POINTER(lyc_layer_cache), I, I]
+    L.lyc_tree_attention.argtypes = [ctypes.POINTER(lyc_layer_cache), ctypes.POINTER(lyc_tree_args), P]
     for name in EXPORTED:
         if name not in ("lyc_status_string", "lyc_last_error", "lyc_destroy"):
             getattr(L, name).restype = I
+    L.lyc_tree_workspace_bytes.restype = ctypes.c_uint64
+    L.lyc_operator_error.restype = ctypes.c_char_p
     _lib = L
     return L
 
@@ -251,6 +302,31 @@ def lyc_last_error(ctx) -> str:
 
 def lyc_destroy(ctx) -> None:
     load().lyc_destroy(ctx)
+
+
+def lyc_qk_norm_rope(args: lyc_rope_args, stream) -> int:
+    return load().lyc_qk_norm_rope(args, stream)
+
+
+def lyc_cache_append(cache: lyc_layer_cache, args: lyc_append_args, stream) -> int:
+    return load().lyc_cache_append(cache, args, stream)
+
+
+def lyc_cache_read(cache: lyc_layer_cache, args: lyc_read_args, stream) -> int:
+    return load().lyc_cache_read(cache, args, stream)
+
+
+def lyc_tree_workspace_bytes(cache: lyc_layer_cache, T: int, num_q_heads: int) -> int:
+    """0 where lyc_tree_attention would refuse the arguments."""
+    return load().lyc_tree_workspace_bytes(cache, T, num_q_heads)
+
+
+def lyc_tree_attention(cache: lyc_layer_cache, args: lyc_tree_args, stream) -> int:
+    return load().lyc_tree_attention(cache, args, stream)
+
+
+def lyc_operator_error() -> str:
+    return load().lyc_operator_error().decode()
 
 
 # ------------------------------------------------------------ torch wrapper
@@ -424,3 +500,306 @@ class Lyc:
         self._check(load().lyc_step_launches(self.ctx, ctypes.byref(a), ctypes.byref(t), ctypes.byref(o)),
                     "lyc_step_launches")
         return a.value, t.value, o.value
+
+
+# ------------------------------------------------------------ serving operators
+#
+# Functions on one layer's torch tensors (include/lyc.h, "Serving operators").
+# Tensors must lie on one device and stay valid until the stream has run the
+# call; `stream` is a torch.cuda.Stream of that device (None: its current
+# stream).  `status`: an int32 or uint32 tensor of one element that collects the
+# LYC_OP_* bits of what only the device can see, or None.  Wrong arguments raise
+# LycError (LYC_ERR_INVALID_ARG or LYC_ERR_UNSUPPORTED) and enqueue nothing.
+
+
+def _refuse(where: str, what: str, code: int = LYC_ERR_INVALID_ARG):
+    raise LycError(code, where, what)
+
+
+def _operator_check(rc: int, where: str):
+    if rc != LYC_OK:
+        raise LycError(rc, where, lyc_operator_error())
+
+
+def _same_device(where, index, **tensors):
+    for name, t in tensors.items():
+        if t is not None and (t.device.type != "cuda" or t.device.index != index):
+            _refuse(where, f"{name} is on {t.device}, not on cuda:{index}")
+
+
+def _typed(where, name, t, dtype, shape):
+    if t.dtype != dtype:
+        _refuse(where, f"{name} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        _refuse(where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+
+
+def _packed(where, name, t, dtype, shape):
+    _typed(where, name, t, dtype, shape)
+    if not t.is_contiguous():
+        _refuse(where, f"{name} must be contiguous")
+
+
+def _rows_in(where, name, t, dtype, shape):
+    _typed(where, name, t, dtype, shape)
+    if t.stride(-1) != 1:
+        _refuse(where, f"{name}: the elements of a row must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_on(index: int, stream) -> int:
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream
+
+
+def _status_ptr(where, status, index):
+    import torch
+    if status is None:
+        return None
+    if status.dtype not in (torch.int32, torch.uint32) or status.numel() != 1 or status.device.index != index:
+        _refuse(where, f"status must be one int32 or uint32 on cuda:{index}")
+    return status.data_ptr()
+
+
+class KvCache:
+    """One layer's cache, described once and handed to cache_append, cache_read
+    and tree_attention (lyc_layer_cache).
+
+      contiguous  k, v [B][Hkv][rows][d]
+      paged       k, v [pages][page_rows][Hkv][d] and block_table int32 [B][max_blocks]
+
+    k and v: bf16, or float8_e4m3fn with k_scale and v_scale of their shape
+    without d (float8_e8m0fnu or uint8 bytes).  Any strides with the d elements
+    of a row contiguous; K and V alike.  The object holds the tensors; it is
+    valid while they are not moved."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None, block_table=None):
+        import torch
+        where = "KvCache"
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            _refuse(where, "k must be a 4-D bf16 or float8_e4m3fn tensor")
+        if k.device.type != "cuda":
+            _refuse(where, f"k is on {k.device}: the cache lies on a GPU")
+        _rows_in(where, "k", k, k.dtype, k.shape)
+        _rows_in(where, "v", v, k.dtype, k.shape)
+        if k.stride() != v.stride():
+            _refuse(where, "k and v must have the same strides")
+        self.e4m3 = k.dtype == torch.float8_e4m3fn
+        self.device_index = k.device.index
+        _same_device(where, self.device_index, v=v, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
+        if (k_scale is None) == self.e4m3 or (v_scale is None) == self.e4m3:
+            _refuse(where, "a float8_e4m3fn cache has scales, a bf16 cache has none")
+        ss = (0, 0, 0)
+        if self.e4m3:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or t.shape != k.shape[:3]:
+                    _refuse(where, f"{name} must be float8_e8m0fnu or uint8 of shape {tuple(k.shape[:3])}")
+            if k_scale.stride() != v_scale.stride():
+                _refuse(where, "k_scale and v_scale must have the same strides")
+            ss = k_scale.stride()
+        st = k.stride()
+        self.tensors = (k, v, k_scale, v_scale, block_table)
+        kind = LYC_CACHE_E4M3 if self.e4m3 else LYC_CACHE_BF16
+        if block_table is None:
+            self.batch, self.heads, rows, self.d = k.shape
+            self.desc = lyc_layer_cache(
+                k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), st[0], st[1], st[2], 0, ss[0], ss[1], ss[2], 0,
+                None, rows, 0, 0, 0, kind, self.batch, self.heads, self.d, self.device_index)
+        else:
+            pages, page_rows, self.heads, self.d = k.shape
+            if block_table.dim() != 2:
+                _refuse(where, "block_table must be [B][max_blocks]")
+            _packed(where, "block_table", block_table, torch.int32, block_table.shape)
+            self.batch = block_table.shape[0]
+            self.desc = lyc_layer_cache(
+                k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), 0, st[2], st[1], st[0], 0, ss[2], ss[1], ss[0],
+                block_table.data_ptr(), 0, pages, page_rows, block_table.shape[1], kind, self.batch, self.heads, self.d,
+                self.device_index)
+
+    @staticmethod
+    def empty(batch, heads, d, rows=None, page_rows=None, num_pages=None, block_table=None, e4m3=True, device="cuda"):
+        """A zeroed cache: contiguous of `rows` rows, or `num_pages` pages of
+        page_rows rows named by block_table."""
+        import torch
+        shape = (batch, heads, rows, d) if block_table is None else (num_pages, page_rows, heads, d)
+        dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        k, v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else dtype, device=device).view(dtype) for _ in range(2))
+        scales = (None, None)
+        if e4m3:
+            # a head's scales lie together: in a page, [Hkv][page_rows]
+            inner = shape[:3] if block_table is None else (num_pages, heads, page_rows)
+            scales = [torch.zeros(inner, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu) for _ in range(2)]
+            if block_table is not None:
+                scales = [t.transpose(1, 2) for t in scales]
+        return KvCache(k, v, *scales, block_table=block_table)
+
+
+def qk_norm_rope(q, k, pos, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                 stream=None):
+    """Per-head RMS norm (where weights are given) and rotation of q [rows][Hq][d]
+    and k [rows][Hkv][d] by pos int32 [rows] and inv_freq fp32 [rot_dim/2] (None:
+    no rotation), into q_out and k_out (lyc_qk_norm_rope).  bf16 or fp32; q and
+    q_out, or k and k_out, may be None; an output may be its input."""
+    import torch
+    where = "qk_norm_rope"
+    x = q if q is not None else k
+    if x is None or x.dim() != 3:
+        _refuse(where, "q or k must be a [rows][heads][d] tensor")
+    index, rows, d, dtype = x.device.index, x.shape[0], x.shape[2], x.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        _refuse(where, f"{dtype} is neither bfloat16 nor float32")
+    _same_device(where, index, q=q, k=k, pos=pos, inv_freq=inv_freq, q_out=q_out, k_out=k_out, q_weight=q_weight,
+                 k_weight=k_weight)
+    st = []
+    for name, a, b, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+        if a is None:
+            if b is not None or w is not None:
+                _refuse(where, f"{name}_out or {name}_weight without {name}")
+            st.append((0, 0, 0, 0, 0))
+            continue
+        if b is None:
+            _refuse(where, f"{name} without {name}_out")
+        shape = (rows, a.shape[1], d) if a.dim() == 3 else (rows, 0, d)
+        _rows_in(where, name, a, dtype, shape)
+        _rows_in(where, name + "_out", b, dtype, shape)
+        if w is not None:
+            _packed(where, name + "_weight", w, dtype, (d,))
+        sa, sb = a.stride(), b.stride()
+        st.append((sa[0], sa[1], sb[0], sb[1], shape[1]))
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _packed(where, "inv_freq", inv_freq, torch.float32, (rot // 2,))
+        if pos is None:
+            _refuse(where, "a rotation needs pos")
+        _packed(where, "pos", pos, torch.int32, (rows,))
+    args = lyc_rope_args(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), st[0][0], st[0][1], st[1][0], st[1][1],
+                         st[0][2], st[0][3], st[1][2], st[1][3], _ptr(pos) if rot else None, _ptr(inv_freq),
+                         _ptr(q_weight), _ptr(k_weight), rows, st[0][4], st[1][4], d, rot, int(interleaved), eps,
+                         LYC_BF16 if dtype == torch.bfloat16 else LYC_FP32, index)
+    _operator_check(lyc_qk_norm_rope(args, _stream_on(index, stream)), "lyc_qk_norm_rope")
+
+
+def cache_append(cache, n, k, v, t_len=None, q=None, q_out=None, pos=None, inv_freq=None, q_weight=None,
+                 k_weight=None, eps=1e-6, interleaved=False, status=None, stream=None):
+    """The last t_len[b] (default T) tokens' k, v [B][T][Hkv][d] bf16 written at
+    rows n[b] - t_len[b] + t of `cache`, quantised where it is e4m3, the keys
+    normed and rotated on the way where k_weight and inv_freq are given, and the
+    same tokens' queries q [B][T][Hq][d] with them into q_out (lyc_cache_append).
+    n, t_len: int32 [B] on the device; pos: int32 [B][T], default the row."""
+    import torch
+    where = "cache_append"
+    index = cache.device_index
+    if k.dim() != 4:
+        _refuse(where, "k must be [B][T][Hkv][d]")
+    T, bf16 = k.shape[1], torch.bfloat16
+    shape = (cache.batch, T, cache.heads, cache.d)
+    _same_device(where, index, n=n, k=k, v=v, t_len=t_len, q=q, q_out=q_out, pos=pos, inv_freq=inv_freq,
+                 q_weight=q_weight, k_weight=k_weight)
+    _rows_in(where, "k", k, bf16, shape)
+    _rows_in(where, "v", v, bf16, shape)
+    _packed(where, "n", n, torch.int32, (cache.batch,))
+    if t_len is not None:
+        _packed(where, "t_len", t_len, torch.int32, (cache.batch,))
+    hq, sq, sqo = 0, (0, 0, 0), (0, 0, 0)
+    if q is not None:
+        if q_out is None or q.dim() != 4:
+            _refuse(where, "q must be [B][T][Hq][d] and have a q_out")
+        hq = q.shape[2]
+        _rows_in(where, "q", q, bf16, (cache.batch, T, hq, cache.d))
+        _rows_in(where, "q_out", q_out, bf16, q.shape)
+        sq, sqo = q.stride(), q_out.stride()
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _packed(where, "inv_freq", inv_freq, torch.float32, (rot // 2,))
+    if pos is not None:
+        _packed(where, "pos", pos, torch.int32, (cache.batch, T))
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _packed(where, name, w, bf16, (cache.d,))
+    sk, sv = k.stride(), v.stride()
+    args = lyc_append_args(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2],
+                           sq[0], sq[1], sq[2], sqo[0], sqo[1], sqo[2], n.data_ptr(), _ptr(t_len), _ptr(pos),
+                           _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), T, hq, rot, int(interleaved), eps,
+                           _status_ptr(where, status, index))
+    _operator_check(lyc_cache_append(cache.desc, args, _stream_on(index, stream)), "lyc_cache_append")
+
+
+def cache_read(cache, n, k_out, v_out, sets=None, first=0, status=None, stream=None):
+    """Rows of `cache` read back, dequantised, into k_out and v_out [B][H][m][d]
+    (bf16 or fp32): rows first .. first+m-1 below n[b] (H = Hkv), or the rows of
+    sets int32 [B][H][m] (H a multiple of Hkv: the step's S) (lyc_cache_read)."""
+    import torch
+    where = "cache_read"
+    index = cache.device_index
+    if k_out.dim() != 4 or k_out.dtype not in (torch.bfloat16, torch.float32):
+        _refuse(where, "k_out must be a [B][H][m][d] bf16 or fp32 tensor")
+    H, m = k_out.shape[1], k_out.shape[2]
+    _same_device(where, index, n=n, k_out=k_out, v_out=v_out, sets=sets)
+    _rows_in(where, "k_out", k_out, k_out.dtype, (cache.batch, H, m, cache.d))
+    _rows_in(where, "v_out", v_out, k_out.dtype, k_out.shape)
+    if k_out.stride() != v_out.stride():
+        _refuse(where, "k_out and v_out must have the same strides")
+    _packed(where, "n", n, torch.int32, (cache.batch,))
+    if sets is not None:
+        _packed(where, "sets", sets, torch.int32, (cache.batch, H, m))
+    so = k_out.stride()
+    args = lyc_read_args(k_out.data_ptr(), v_out.data_ptr(), so[0], so[1], so[2], n.data_ptr(), _ptr(sets), int(first),
+                         m, H, LYC_BF16 if k_out.dtype == torch.bfloat16 else LYC_FP32,
+                         _status_ptr(where, status, index))
+    _operator_check(lyc_cache_read(cache.desc, args, _stream_on(index, stream)), "lyc_cache_read")
+
+
+def tree_attention(q, cache, n, out, mask=None, t_len=None, scale=None, workspace=None, status=None, stream=None):
+    """Attention of the last t_len[b] (default T) of n[b] rows' queries q
+    [B][T][Hq][d] over `cache` into out (lyc_tree_attention): every row before
+    the drafted ones, and the drafted nodes of mask int64 [B][T][ceil(T/64)]
+    (None: a chain; T = 1: one token's dense attention).  scale: default
+    d ** -0.5.  workspace: a device tensor of tree_workspace_bytes(...) bytes
+    that no other call uses meanwhile; by default one is taken from torch's
+    allocator for this call."""
+    import torch
+    where = "tree_attention"
+    index = cache.device_index
+    if q.dim() != 4:
+        _refuse(where, "q must be [B][T][Hq][d]")
+    T, hq = q.shape[1], q.shape[2]
+    _same_device(where, index, q=q, n=n, out=out, mask=mask, t_len=t_len, workspace=workspace)
+    _rows_in(where, "q", q, torch.bfloat16, (cache.batch, T, hq, cache.d))
+    _rows_in(where, "out", out, torch.bfloat16, q.shape)
+    _packed(where, "n", n, torch.int32, (cache.batch,))
+    if t_len is not None:
+        _packed(where, "t_len", t_len, torch.int32, (cache.batch,))
+    if mask is not None:
+        if mask.dtype not in (torch.int64, torch.uint64):
+            _refuse(where, f"mask is {mask.dtype}, not int64")
+        _packed(where, "mask", mask, mask.dtype, (cache.batch, T, -(-T // 64)))
+    if workspace is None:
+        need = tree_workspace_bytes(cache, T, hq)
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            with torch.cuda.stream(stream):  # the allocator orders its reuse on the call's stream
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        _refuse(where, "workspace must be contiguous")
+    sq, so = q.stride(), out.stride()
+    args = lyc_tree_args(q.data_ptr(), out.data_ptr(), sq[0], sq[1], sq[2], so[0], so[1], so[2], n.data_ptr(),
+                         _ptr(t_len), _ptr(mask), T, hq, cache.d**-0.5 if scale is None else scale,
+                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                         _status_ptr(where, status, index))
+    _operator_check(lyc_tree_attention(cache.desc, args, _stream_on(index, stream)), "lyc_tree_attention")
+
+
+def tree_workspace_bytes(cache, T: int, num_q_heads: int) -> int:
+    """Bytes of tree_attention's workspace for q [B][T][num_q_heads][d] over `cache`."""
+    need = lyc_tree_workspace_bytes(cache.desc, T, num_q_heads)
+    if need == 0:
+        raise LycError(LYC_ERR_INVALID_ARG, "lyc_tree_workspace_bytes", lyc_operator_error())
+    return need

@@ -394,6 +394,192 @@ lyc_status lyc_sparse_attention_noalloc(const void* q, const lyc_kv_cache* kv, i
                                         const int32_t* S, int k, float* out, uint32_t* status,
                                         void* stream);
 
+/* ---- Serving operators (no counterpart in the paper).
+ *
+ * What a program does on either side of the decode step, for ONE layer per
+ * call: the per-head norm and the rotation of a step's queries and keys, the
+ * cache written in 8 bits (or bf16) as its rows are made, rows of it read
+ * back, and dense attention of one or several drafted tokens over it.
+ *
+ * These entry points hold no context and no scratch of their own and allocate
+ * nothing: tensors, workspace and status word are the caller's, all on device
+ * `device` of the argument struct.  They are asynchronous on `stream` (a
+ * cudaStream_t of that device, NULL = legacy default stream), may be captured
+ * into a CUDA graph, and may be called from several host threads.  Calls that
+ * overlap on the GPU must not share outputs, rows being written, or a
+ * workspace.  Inputs may not overlap outputs except where said.  All strides
+ * are in elements of their tensor; the head_dim elements of a row are
+ * contiguous, and every row starts on a 16-byte boundary (pointers 16-byte
+ * aligned, strides multiples of 16 bytes; LYC_ERR_INVALID_ARG otherwise).
+ * Strides are >= 0.  Where a dimension has one entry its stride is not used.
+ *
+ * Errors found on the host are returned at once, nothing is enqueued, and
+ * lyc_operator_error() has the reason.  What only the device can see (a
+ * length, a page or an index out of range) is skipped, touches no memory, and
+ * sets a bit of *status, a device uint32 that the caller clears (or NULL):
+ *   LYC_OP_BAD_LENGTH  an element whose n and t_len do not satisfy
+ *                      0 <= t_len <= T and t_len <= n <= capacity: the element
+ *                      is left out, its outputs and rows as they were
+ *   LYC_OP_BAD_PAGE    a block-table entry outside [0, num_pages) among the
+ *                      rows used: not written; read as absent (tree attention:
+ *                      the row is not seen; read: the output row as it was)
+ *   LYC_OP_BAD_INDEX   a set index outside [-1, n): the output row as it was */
+#define LYC_OP_BAD_LENGTH 0x1u
+#define LYC_OP_BAD_PAGE 0x2u
+#define LYC_OP_BAD_INDEX 0x4u
+
+/* How a layer's cache holds its rows.  LYC_CACHE_E4M3: element j of a row is
+ * codes[j] * 2^(scale - 127): 8-bit e4m3 codes and one E8M0 scale byte for
+ * each (element, KV head, row), for K and V apart.  The writer takes the
+ * smallest power of two 2^e, -100 <= e, with max|x| <= 448 * 2^e, so that a
+ * code is x * 2^-e rounded once (to nearest, ties to even) and reading back
+ * is exact in bf16 (within its range: magnitudes of 1.9375 * 2^127 and more
+ * read back as infinite, and what is below its smallest number rounds).  A row that holds a NaN or
+ * an infinity gets scale byte 255 and zero codes and reads back as NaN.
+ * Codes 0x7f and 0xff (NaN) are never written and are not looked for. */
+typedef enum { LYC_CACHE_BF16 = 0, LYC_CACHE_E4M3 = 1 } lyc_cache_type;
+
+/* One layer's cache.  Row i of (element b, KV head g):
+ *   contiguous (block_table == NULL): element b*s_batch + g*s_head + i*s_token,
+ *     i < rows;
+ *   paged: p = block_table[b*max_blocks + i/page_rows], element
+ *     p*s_page + (i % page_rows)*s_token + g*s_head, i < max_blocks*page_rows.
+ * The scale bytes lie the same way with the ss_ strides (any alignment).
+ * The capacity (rows, or max_blocks*page_rows) is at most 2^30.  page_rows may
+ * be any number >= 1.  Pages written must be used by one element only. */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale; /* E4M3 only, else NULL */
+  uint8_t* v_scale;
+  int64_t s_batch, s_head, s_token, s_page;
+  int64_t ss_batch, ss_head, ss_token, ss_page;
+  const int32_t* block_table; /* device [batch][max_blocks], or NULL */
+  int64_t rows;               /* contiguous: rows allocated for each element */
+  int64_t num_pages;
+  int32_t page_rows, max_blocks;
+  int32_t type; /* lyc_cache_type */
+  int32_t batch, num_kv_heads, head_dim; /* head_dim 64 or 128 */
+  int32_t device;
+} lyc_layer_cache;
+
+/* Norms of queries and keys for each head and the rotation by position, in
+ * one pass: for every row r and head h, x = q[r][h] (k[r][h]),
+ *   y = x * rsqrt(mean(x^2) + eps) * weight        (weight NULL: y = x),
+ *   angle_i = pos[r] * inv_freq[i], i < rot_dim/2, taken in 64 bits;
+ *   pairs (i, i + rot_dim/2), or with `interleaved` (2i, 2i+1), of y turned by
+ *   it: (a cos - b sin, b cos + a sin); elements past rot_dim as they are.
+ * Sums, norms and products in fp32, one rounding at the end.  rot_dim: 0 (no
+ * rotation; pos and inv_freq are not read and may be NULL) or a multiple of
+ * 16 up to head_dim.  A row with pos < 0 is padding: not read, outputs as
+ * they were.  q or k may be NULL (with its outputs).  q_out may be q with the
+ * same strides, k_out k (in place).  weights: [head_dim] of `dtype`.
+ * rows == 0 does nothing. */
+typedef struct {
+  const void* q; /* [rows][num_q_heads][head_dim] of dtype */
+  const void* k; /* [rows][num_kv_heads][head_dim] */
+  void* q_out;
+  void* k_out;
+  int64_t q_row, q_head, k_row, k_head;         /* strides */
+  int64_t qo_row, qo_head, ko_row, ko_head;
+  const int32_t* pos;    /* device [rows] */
+  const float* inv_freq; /* device [rot_dim/2] */
+  const void* q_weight;  /* device [head_dim], or NULL */
+  const void* k_weight;
+  int64_t rows;
+  int32_t num_q_heads, num_kv_heads, head_dim, rot_dim, interleaved;
+  float eps;
+  int32_t dtype; /* lyc_dtype */
+  int32_t device;
+} lyc_rope_args;
+lyc_status lyc_qk_norm_rope(const lyc_rope_args* args, void* stream);
+
+/* The keys and values of the last t_len[b] tokens of every element (T of them
+ * where t_len is NULL) written into the cache, at rows n[b]-t_len[b]+t:
+ * n[b] counts them, as everywhere in this library.  On the way the keys can
+ * be normed and rotated, and the queries of the same tokens with them, as in
+ * lyc_qk_norm_rope, at position pos[b][t] or, where pos is NULL, the row's
+ * number (no rotation: rot_dim 0; a negative pos counts as its angle says, it
+ * pads nothing here).  K is quantised from the fp32 values.  Rows t >=
+ * t_len[b] are padding: not read, outputs as they were.  bf16 tensors.
+ * Rows [n-t_len, n) of the cache are written, no other byte of it. */
+typedef struct {
+  const void* k; /* [batch][T][num_kv_heads][head_dim] bf16 */
+  const void* v;
+  const void* q; /* [batch][T][num_q_heads][head_dim] bf16, or NULL */
+  void* q_out;   /* the same shape; may be q with the same strides */
+  int64_t k_batch, k_token, k_head, v_batch, v_token, v_head;
+  int64_t q_batch, q_token, q_head, qo_batch, qo_token, qo_head;
+  const int32_t* n;      /* device [batch] */
+  const int32_t* t_len;  /* device [batch], or NULL */
+  const int32_t* pos;    /* device [batch][T], or NULL */
+  const float* inv_freq; /* device [rot_dim/2], or NULL with rot_dim 0 */
+  const void* q_weight;  /* device [head_dim] bf16, or NULL */
+  const void* k_weight;
+  int32_t T, num_q_heads, rot_dim, interleaved;
+  float eps;
+  uint32_t* status;
+} lyc_append_args;
+lyc_status lyc_cache_append(const lyc_layer_cache* cache, const lyc_append_args* args, void* stream);
+
+/* Rows of the cache read back (E4M3: dequantised) into k_out and v_out
+ * [batch][H][m][head_dim], bf16 or fp32.
+ *   sets == NULL: H = num_kv_heads, entry i is row first + i; entries at or
+ *     past n[b] are left as they were;
+ *   sets: device [batch][H][m] int32, H a multiple of num_kv_heads (Hkv or Hq:
+ *     the step's S), entry i is row sets[b][h][i] of KV head h / (H / Hkv); -1
+ *     entries are left as they were. */
+typedef struct {
+  void* k_out;
+  void* v_out;
+  int64_t o_batch, o_head, o_row; /* strides of both */
+  const int32_t* n;               /* device [batch] */
+  const int32_t* sets;
+  int64_t first;
+  int32_t m, num_heads;
+  int32_t dtype; /* lyc_dtype of the outputs */
+  uint32_t* status;
+} lyc_read_args;
+lyc_status lyc_cache_read(const lyc_layer_cache* cache, const lyc_read_args* args, void* stream);
+
+/* Attention of a tree of drafted tokens over the cache.  The last t_len[b]
+ * rows (T where t_len is NULL) of element b's n[b] rows are the drafted
+ * nodes; query t of head h sees every row before them and node j where bit j
+ * of its mask is set:
+ *   out[b][t][h] = softmax(scale * q[b][t][h] . K^T) V over the rows seen,
+ * zero where none is seen.  mask: device [batch][T][W] 64-bit words, W =
+ * ceil(T / 64), bit j of a row = word j/64, bit j%64 (a node sees itself only
+ * where its own bit is set; bits at or past t_len are not looked at); NULL: a
+ * chain, node t sees nodes 0..t (T = 1: the dense decode of one token).  What
+ * lies in rows not seen, NaN included, does not reach the output.  Queries
+ * t >= t_len[b] are padding: not read, outputs as they were.  1 <= T <= 256.
+ * Scores, sums and the softmax are fp32; the probabilities are rounded to the
+ * 16-bit type of the second product.  The result of a call does not depend on
+ * the order in which the GPU runs its blocks.
+ *   q, out  [batch][T][num_q_heads][head_dim] bf16, num_q_heads a multiple of
+ *           num_kv_heads
+ *   workspace  device, lyc_tree_workspace_bytes(...) bytes, 16-byte aligned,
+ *           any contents; used while the call runs */
+typedef struct {
+  const void* q;
+  void* out;
+  int64_t q_batch, q_token, q_head, o_batch, o_token, o_head;
+  const int32_t* n;      /* device [batch] */
+  const int32_t* t_len;  /* device [batch], or NULL */
+  const uint64_t* mask;  /* device [batch][T][W], or NULL */
+  int32_t T, num_q_heads;
+  float scale; /* > 0; the usual one is 1/sqrt(head_dim) */
+  void* workspace;
+  uint64_t workspace_bytes;
+  uint32_t* status;
+} lyc_tree_args;
+/* 0 for arguments that lyc_tree_attention refuses. */
+uint64_t lyc_tree_workspace_bytes(const lyc_layer_cache* cache, int T, int num_q_heads);
+lyc_status lyc_tree_attention(const lyc_layer_cache* cache, const lyc_tree_args* args, void* stream);
+
+/* Why this thread's last failing serving operator failed ("" if none did). */
+const char* lyc_operator_error(void);
+
 const char* lyc_status_string(lyc_status s);
 const char* lyc_last_error(const lyc_ctx* ctx);
 void lyc_destroy(lyc_ctx* ctx);
