@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "liblyc.so")
 SOURCES = ["attn_kernel.cu", "attn_mma_kernel.cu", "topk_kernel.cu", "misc_kernels.cu", "lyc_api.cu", "noalloc.cu", "attn_tc_kernel.cu", "correction_kernel.cu",
-           "token_kernels.cu", "tree_mma_kernel.cu", "serve_api.cu"]
+           "token_kernels.cu", "tree_mma_kernel.cu", "tree_tc_kernel.cu", "serve_api.cu"]
 HEADERS = ["lyc_plan.h", "lyc_device.cuh", "tc_ptx.cuh", "serve_plan.h", "tree_sched.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",

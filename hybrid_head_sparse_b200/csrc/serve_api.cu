@@ -137,18 +137,22 @@ int sm_count(int device) {
   return sms;
 }
 
+constexpr int kMmaMostRows = 32;
+
 struct TreeShape {
+  bool tc;  // the tcgen05 kernel
   int block_rows, tile_rows, mblocks, grid;
   int64_t cap_tiles;  // tiles of a group at the cache's capacity
   uint64_t bytes;
 };
 
-bool tree_shape(const lyc_layer_cache* c, int T, int Hq, TreeShape* s) {
+bool tree_shape(const lyc_layer_cache* c, int T, int Hq, bool may_tc, TreeShape* s) {
   const int sms = sm_count(c->device);
   if (sms < 1) return false;
   const int rows = Hq / c->num_kv_heads * T;
-  s->block_rows = tree_mma_block_rows(rows);
-  s->tile_rows = tree_mma_tile_rows(c->head_dim, c->type);
+  s->tc = may_tc && c->head_dim == 128 && rows > kMmaMostRows && tree_tc_box_rows(view(c)) > 0;
+  s->block_rows = s->tc ? 128 : tree_mma_block_rows(rows);
+  s->tile_rows = s->tc ? 128 : tree_mma_tile_rows(c->head_dim, c->type);
   s->mblocks = (rows + s->block_rows - 1) / s->block_rows;
   const int64_t cap = view(c).cap;
   s->cap_tiles = (cap + s->tile_rows - 1) / s->tile_rows;
@@ -349,7 +353,7 @@ lyc_status lyc_cache_read(const lyc_layer_cache* c, const lyc_read_args* a, void
 uint64_t lyc_tree_workspace_bytes(const lyc_layer_cache* c, int T, int num_q_heads) {
   if (check_tree(c, T, num_q_heads) != LYC_OK) return 0;
   TreeShape s;
-  if (!tree_shape(c, T, num_q_heads, &s)) {
+  if (!tree_shape(c, T, num_q_heads, true, &s)) {
     refuse(LYC_ERR_CUDA, "device %d cannot be used", c->device);
     return 0;
   }
@@ -371,13 +375,14 @@ lyc_status lyc_tree_attention(const lyc_layer_cache* c, const lyc_tree_args* a, 
     return refuse(LYC_ERR_INVALID_ARG, "rows of out overlap");
   OnDevice on(c->device);
   TreeShape s;
-  if (!on.ok || !tree_shape(c, a->T, a->num_q_heads, &s))
+  if (!on.ok || !tree_shape(c, a->T, a->num_q_heads, true, &s))
     return refuse(LYC_ERR_CUDA, "device %d cannot be used", c->device);
   if (!a->workspace || misaligned(a->workspace) || a->workspace_bytes < s.bytes)
     return refuse(LYC_ERR_INVALID_ARG, "the workspace needs %llu bytes, 16-byte aligned",
                   static_cast<unsigned long long>(s.bytes));
-  TreeParams p;
-  memset(&p, 0, sizeof p);
+  TreeTcParams P;
+  memset(&P, 0, sizeof P);
+  TreeParams& p = P.t;
   p.q = static_cast<const unsigned char*>(a->q);
   p.out = static_cast<unsigned char*>(a->out);
   p.q_batch = a->q_batch;
@@ -396,14 +401,19 @@ lyc_status lyc_tree_attention(const lyc_layer_cache* c, const lyc_tree_args* a, 
   p.Hq = a->num_q_heads;
   p.Hkv = c->num_kv_heads;
   p.G = a->num_q_heads / c->num_kv_heads;
-  p.mblocks = s.mblocks;
-  p.grid = s.grid;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.cache = view(c);
+  if (s.tc) {
+    p.box_rows = tree_tc_box_rows(p.cache);
+    // a layout that TMA cannot describe (a stride of 2^40 bytes, say); needs no more workspace
+    if (!tree_tc_maps(&P, c->type)) tree_shape(c, a->T, a->num_q_heads, false, &s);
+  }
+  p.grid = s.grid;
   p.part_o = static_cast<float*>(a->workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2ll * s.grid * s.block_rows * c->head_dim);
   const cudaStream_t str = static_cast<cudaStream_t>(stream);
-  lyc_status rc = launched(tree_mma_launch(&p, c->head_dim, c->type, s.block_rows, c->device, str),
+  lyc_status rc = launched(s.tc ? tree_tc_launch(&P, c->type, c->device, str)
+                                : tree_mma_launch(&p, c->head_dim, c->type, s.block_rows, c->device, str),
                            "tree attention launch");
   // a group of one tile is never cut: nothing to merge
   if (rc == LYC_OK && s.cap_tiles > 1)

@@ -2,6 +2,7 @@
 // "Serving operators"): token_kernels.cu, tree_mma_kernel.cu; filled in by
 // serve_api.cu.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -93,10 +94,15 @@ struct TreeParams {
   float* part_o;    // [2 * grid][rows per block][d]
   float2* part_ml;  // [2 * grid][rows per block]: running maximum (log2 units) and sum
   int32_t B, T, W, Hq, Hkv, G;
-  int32_t mblocks;  // blocks of query rows of a group
   int32_t grid;
+  int32_t box_rows;  // tcgen05 kernel: rows of one TMA box
   float scale_log2;
   CacheView cache;
+};
+
+struct TreeTcParams {
+  CUtensorMap tmk, tmv;
+  TreeParams t;
 };
 
 // token_kernels.cu
@@ -108,6 +114,10 @@ int tree_mma_tile_rows(int head_dim, int cache_type);
 int tree_mma_block_rows(int rows);
 cudaError_t tree_mma_launch(const TreeParams* p, int head_dim, int cache_type, int block_rows, int device,
                             cudaStream_t stream);
+// tree_tc_kernel.cu: head_dim 128; 128 rows a tile, 128 query rows a block
+int tree_tc_box_rows(const CacheView& c);
+bool tree_tc_maps(TreeTcParams* P, int cache_type);
+cudaError_t tree_tc_launch(const TreeTcParams* P, int cache_type, int device, cudaStream_t stream);
 cudaError_t tree_combine_launch(const TreeParams* p, int head_dim, int block_rows, int tile_rows,
                                 cudaStream_t stream);
 

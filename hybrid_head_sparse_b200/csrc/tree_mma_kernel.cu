@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
       tree_elem(p, b, &bad);
       if (bad) atomicOr(p.status, LYC_OP_BAD_LENGTH);
     }
-  const TreeSched<C::TR> sched(p);
+  const TreeSched<C::TR, C::ROWS> sched(p);
   const int cta = blockIdx.x;
   const int64_t xbeg = sched.begin(cta), xend = sched.begin(cta + 1);
   const float NEG = -INFINITY;
@@ -259,8 +259,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
     const int nt = (pc.e.n + C::TR - 1) / C::TR;
     const int64_t rel = x - efirst;
     const int grp = static_cast<int>(rel / nt);
-    pc.g = grp / p.mblocks;
-    pc.mb = grp % p.mblocks;
+    const int mbs = sched.blocks(pc.e);
+    pc.g = grp / mbs;
+    pc.mb = grp % mbs;
     pc.t0 = static_cast<int>(rel - static_cast<int64_t>(grp) * nt);
     pc.t1 = static_cast<int>(min(static_cast<int64_t>(nt), pc.t0 + (xend - x)));
     x += pc.t1 - pc.t0;
@@ -634,7 +635,7 @@ template <int D, int ROWS, int TR>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeParams p) {
   const int lane = threadIdx.x & 31;
   pdl_wait();
-  const TreeSched<TR> sched(p);
+  const TreeSched<TR, ROWS> sched(p);
   if (sched.total == 0) return;
   const int rows = p.G * p.T;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
   if (t >= e.cnt) return;
   const int mb = i / ROWS, row = i % ROWS;
   const int nt = (e.n + TR - 1) / TR;
-  const int64_t x0 = sched.first_tile(static_cast<int>(b)) + static_cast<int64_t>(g * p.mblocks + mb) * nt;
+  const int64_t x0 = sched.first_tile(static_cast<int>(b)) + static_cast<int64_t>(g * sched.blocks(e) + mb) * nt;
   const int c0 = sched.owner(x0), c1 = sched.owner(x0 + nt - 1);
   if (c0 == c1) return;  // its CTA wrote the output
   constexpr int V = D / 32;
@@ -745,6 +746,7 @@ cudaError_t tree_mma_launch(const TreeParams* p, int head_dim, int cache_type, i
 
 cudaError_t tree_combine_launch(const TreeParams* p, int head_dim, int block_rows, int tile_rows,
                                 cudaStream_t stream) {
+  if (block_rows == 128) return launch_combine<128, 128, 128>(p, stream);  // tcgen05 kernel
 #define LYC_COMBINE(DD, TT) \
   (block_rows == 16 ? launch_combine<DD, 16, TT>(p, stream) : launch_combine<DD, 32, TT>(p, stream))
   if (head_dim == 128) return tile_rows == 128 ? LYC_COMBINE(128, 128) : LYC_COMBINE(128, 256);

@@ -2,9 +2,8 @@
 // launch, computed on the device from the elements' lengths (so that one
 // captured graph serves every length up to the cache's capacity).
 //
-// A group is one (element b, KV head g, block mb of its query rows); it has
-// nt(b) = ceil(n[b] / tile rows) tiles of the cache, or none where the element
-// has no queries.  The tiles of all groups, in order, are cut into `grid`
+// A group is one (element b, KV head g, block mb of its G * t_len[b] query
+// rows); it has nt(b) = ceil(n[b] / tile rows) tiles of the cache.  The tiles of all groups, in order, are cut into `grid`
 // equal runs, one for each CTA (with fewer tiles than CTAs, the CTAs past the
 // last tile have none: a CTA inside a cut group always has a slot).  A run holds whole groups, whose outputs its
 // CTA writes, and at most two cut ones: the end of a group begun by an earlier
@@ -33,20 +32,21 @@ __device__ __forceinline__ TreeElem tree_elem(const TreeParams& p, int b, bool* 
 }
 
 // Called by whole warps; every lane gets the result.
-template <int TR>
+template <int TR, int ROWS>
 struct TreeSched {
   const TreeParams& p;
   int64_t total;
-  int gpe;   // groups of an element
   int grid;  // CTAs that have tiles
 
   __device__ __forceinline__ int64_t elem_tiles(int b) const {
     if (b >= p.B) return 0;
     bool bad = false;
     const TreeElem e = tree_elem(p, b, &bad);
-    return e.cnt > 0 ? static_cast<int64_t>((e.n + TR - 1) / TR) * gpe : 0;
+    return static_cast<int64_t>((e.n + TR - 1) / TR) * p.Hkv * blocks(e);
   }
-  __device__ __forceinline__ explicit TreeSched(const TreeParams& prm) : p(prm), gpe(prm.Hkv * prm.mblocks) {
+  // blocks of query rows of a KV head
+  __device__ __forceinline__ int blocks(const TreeElem& e) const { return (e.cnt * p.G + ROWS - 1) / ROWS; }
+  __device__ __forceinline__ explicit TreeSched(const TreeParams& prm) : p(prm) {
     int64_t s = 0;
     const int lane = threadIdx.x & 31;
     for (int b0 = 0; b0 < p.B; b0 += 32) s += elem_tiles(b0 + lane);

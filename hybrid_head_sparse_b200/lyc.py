@@ -57,6 +57,7 @@ LYC_CACHE_E4M3 = 1
 LYC_OP_BAD_LENGTH = 0x1
 LYC_OP_BAD_PAGE = 0x2
 LYC_OP_BAD_INDEX = 0x4
+LYC_OP_TIMEOUT = 0x8
 
 EXPORTED = ["lyc_create", "lyc_decode_step", "lyc_decode_step_host", "lyc_decode_step_batch",
             "lyc_sync_status",

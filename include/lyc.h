@@ -427,6 +427,7 @@ lyc_status lyc_sparse_attention_noalloc(const void* q, const lyc_kv_cache* kv, i
 #define LYC_OP_BAD_LENGTH 0x1u
 #define LYC_OP_BAD_PAGE 0x2u
 #define LYC_OP_BAD_INDEX 0x4u
+#define LYC_OP_TIMEOUT 0x8u /* a device-side wait gave up: the call's outputs are undefined */
 
 /* How a layer's cache holds its rows.  LYC_CACHE_E4M3: element j of a row is
  * codes[j] * 2^(scale - 127): 8-bit e4m3 codes and one E8M0 scale byte for

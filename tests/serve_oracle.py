@@ -89,7 +89,9 @@ def tree(q, cache, n, t_len, mask, scale):
     Bound: each probability carries its rounding u (fp16 or bf16) and e^delta - 1,
     delta what fp32 does to a logit: d + 8 roundoffs of sum |q k| scale, and four of
     the logit in log2 units (at most 1.5 times it, plus 130 for a scale's
-    exponent); the output its own rounding."""
+    exponent); over an e4m3 cache also what a query's elements lose in two e4m3 terms
+    beside the row's largest M (a power of two below it): elements under 2^-9 M are
+    off by 2^-17 M at most, the others are exact; the output its own rounding."""
     q = q.detach().cpu().double()
     B, T, Hq, d = q.shape
     G = Hq // cache.heads
@@ -121,7 +123,12 @@ def tree(q, cache, n, t_len, mask, scale):
                 o[t] = p[t, vis[t]] @ v[vis[t]]
             a = p.nan_to_num() @ v.abs().nan_to_num(posinf=0.0)
             mag = (q[b, :cnt, h].abs() @ k.abs().nan_to_num(posinf=0.0).T * scale).amax(-1, keepdim=True)
-            delta = (d + 8) * U32 * mag + 4 * U32 * (1.5 * mag + (130 if cache.e4m3 else 0)) + 8 * U32
+            lost = 0.0
+            if cache.e4m3:
+                top_q = torch.exp2(torch.floor(torch.log2(q[b, :cnt, h].abs().amax(-1, keepdim=True).clamp(min=1e-300))))
+                small = (q[b, :cnt, h].abs() < 2.0**-9 * top_q).double() * 2.0**-17 * top_q
+                lost = (small @ k.abs().nan_to_num(posinf=0.0).T * scale).amax(-1, keepdim=True)
+            delta = lost + (d + 8) * U32 * mag + 4 * U32 * (1.5 * mag + (130 if cache.e4m3 else 0)) + 8 * U32
             out[b, :cnt, h] = o
             bound[b, :cnt, h] = a * (u + 2 * torch.expm1(delta)) * (1 + 2 * UB) + UB * o.abs() * (1 + UB)
     return out, bound

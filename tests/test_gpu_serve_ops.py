@@ -390,7 +390,8 @@ def test_tree_one_token_every_length(lyc, e4m3, d):
 @pytest.mark.parametrize("T,hq,hkv,d,page", [
     (2, 4, 2, 128, 0), (3, 5, 1, 64, 5), (16, 8, 2, 128, 64), (17, 16, 2, 64, 16), (5, 16, 1, 128, 48),
     (63, 4, 4, 128, 1), (64, 8, 2, 128, 16), (65, 2, 1, 64, 128), (130, 4, 2, 128, 0), (256, 2, 2, 64, 64),
-    (12, 32, 8, 128, 64), (33, 12, 3, 128, 256),
+    (12, 32, 8, 128, 64), (33, 12, 3, 128, 256), (20, 8, 2, 128, 8), (40, 4, 1, 128, 24), (256, 8, 2, 128, 192),
+    (48, 6, 6, 128, 0), (9, 64, 1, 128, 0), (9, 64, 1, 128, 12),
 ])
 def test_tree_shapes(lyc, e4m3, T, hq, hkv, d, page):
     """Trees of every size over ragged lengths: n = t (no prefix), drafts across
@@ -409,14 +410,14 @@ def test_tree_shapes(lyc, e4m3, T, hq, hkv, d, page):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_tree_long_and_split(lyc, e4m3):
+@pytest.mark.parametrize("T", [8, 16, 60])
+def test_tree_long_and_split(lyc, e4m3, T):
     """One element cut over many CTAs beside short ones; the same call twice is
     the same to the bit; a peaked softmax whose tail matters."""
-    n, T = [20000, 3, 5000, 1], 8
     cache = fill(lyc, 4, 2, 128, 20000, 64, e4m3, seed=3)
+    n, t_len = [20000, T, 5000, 1], [T, min(3, T), T - 1, 1]
     poison_past(cache, n)
     q = randn(5, 4, T, 8, 128, scale=2.0)
-    t_len = [8, 3, 5, 1]
     mask = random_tree(np.random.default_rng(1), 4, T)
     a = check_tree(lyc, cache, q, n, t_len, mask, what="long")
     b, _ = run_tree(lyc, cache, q, n, t_len, mask)
@@ -463,27 +464,31 @@ def test_tree_without_anything_to_see(lyc):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-def test_tree_bad_pages_and_lengths(lyc, e4m3):
+@pytest.mark.parametrize("page,hq", [(20, 4), (20, 16), (8, 16), (16, 32)])
+def test_tree_bad_pages_and_lengths(lyc, e4m3, page, hq):
     """Lengths that do not fit leave an element out; rows on pages outside the
     pool are not seen; both are reported."""
-    cache = fill(lyc, 6, 2, 128, 300, 20, e4m3, seed=4)
+    cap = 300 // page * page
+    cache = fill(lyc, 6, 2, 128, cap, page, e4m3, seed=4)
+    poison_past(cache, [min(290, cap), 0, 0, 0, 0, 0])
     bt = cache.tensors[4]
     bt[0, 3] = -5
-    bt[0, 14] = 2**31 - 1  # holds drafted rows
-    q = randn(1, 6, 7, 4, 128)
-    n, t_len = [290, 301, 5, -1, 100, 50], [7, 7, 6, 0, 8, -1]
+    bt[0, 286 // page] = 2**31 - 1  # holds drafted rows
+    q = randn(1, 6, 7, hq, 128)
+    n, t_len = [min(290, cap), 301, 5, -1, 100, 50], [7, 7, 6, 0, 8, -1]
     out, st = run_tree(lyc, cache, q, n, t_len)
     assert st == lyc.LYC_OP_BAD_LENGTH | lyc.LYC_OP_BAD_PAGE
     assert bool((out[1:] == 1234.0).all())
-    w, bd = SO.tree(q[:1], cache, [290], [7], None, 128**-0.5)
+    w, bd = SO.tree(q[:1], cache, n[:1], [7], None, 128**-0.5)
     SO.close(out[:1], w, bd, "rows on bad pages")
 
 
-def test_tree_query_values(lyc):
+@pytest.mark.parametrize("T", [8, 70])
+def test_tree_query_values(lyc, T):
     """Queries of extreme size, zero, NaN and infinity, over both caches."""
     for e4m3 in (False, True):
         cache = fill(lyc, 1, 1, 128, 200, 0, e4m3, seed=6)
-        q = randn(2, 1, 8, 1, 128)
+        q = randn(2, 1, T, 1, 128)
         q[0, 0] = 0
         q[0, 1] *= 2.0**-120
         q[0, 2] *= 2.0**20
@@ -493,33 +498,34 @@ def test_tree_query_values(lyc):
         out, _ = run_tree(lyc, cache, q, [200])
         assert torch.isnan(out[0, 3]).all() and torch.isnan(out[0, 4]).all()
         ok = [0, 1, 2, 5, 6, 7]
-        want, bound = SO.tree(q.nan_to_num(), cache, [200], [8], None, 128**-0.5)
+        want, bound = SO.tree(q.nan_to_num(), cache, [200], [T], None, 128**-0.5)
         # a logit of 2^20 has an absolute error beyond the softmax: hardest row only finite
         assert torch.isfinite(out[0, ok].float()).all()
         for t in (0, 1, 5, 6, 7):
             SO.close(out[0, t], want[0, t], bound[0, t], f"query {t}")
 
 
-def test_tree_strides_streams_graphs(lyc):
+@pytest.mark.parametrize("T", [6, 24])
+def test_tree_strides_streams_graphs(lyc, T):
     """Queries inside a projection's output, heads-first outputs, another stream, a
     captured call replayed at other lengths, and two captured calls at once."""
-    B, T, hq, hkv, d, cap = 2, 6, 8, 2, 128, 3000
+    B, hq, hkv, d, cap = 2, 8, 2, 128, 3000
     cache = fill(lyc, B, hkv, d, cap, 0, True, seed=9)
     qkv = randn(4, B, T, (hq + 4) * d)
     q = qkv[..., 2 * d: (2 + hq) * d].unflatten(2, (hq, d))
     out_t = torch.full((B, hq, T, d), 1234.0, dtype=BF, device="cuda")
-    ref, _ = run_tree(lyc, cache, q, [3000, 17])
-    run_tree(lyc, cache, q, [3000, 17], out=out_t.transpose(1, 2))
+    ref, _ = run_tree(lyc, cache, q, [3000, 27])
+    run_tree(lyc, cache, q, [3000, 27], out=out_t.transpose(1, 2))
     assert torch.equal(out_t.transpose(1, 2), ref)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     out_s = torch.zeros_like(ref)
-    n = i32([3000, 17])
+    n = i32([3000, 27])
     lyc.tree_attention(q, cache, n, out_s, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(out_s, ref)
     # two graphs, each with its own workspace, replayed on two streams at once
-    lens = [i32([3000, 17]), i32([100, 2999])]
+    lens = [i32([3000, 27]), i32([100, 2999])]
     outs = [torch.zeros_like(ref) for _ in range(2)]
     graphs = []
     torch.cuda.synchronize()
@@ -529,7 +535,7 @@ def test_tree_strides_streams_graphs(lyc):
             lyc.tree_attention(q, cache, lens[i], outs[i])
         graphs.append(g)
     streams = [torch.cuda.Stream() for _ in range(2)]
-    for lengths in ([[3000, 17], [100, 2999]], [[7, 6], [1500, 1000]], [[128, 129], [6, 6]]):
+    for lengths in ([[3000, 27], [100, 2999]], [[T + 1, T], [1500, 1000]], [[128, 129], [T, T]]):
         for i in range(2):
             lens[i].copy_(i32(lengths[i]))
         torch.cuda.synchronize()
