@@ -146,6 +146,15 @@ struct TreeShape {
   uint64_t bytes;
 };
 
+// The division of the work counts tiles (and rows of query blocks) in 32 bits.
+bool tree_too_large(const lyc_layer_cache* c, int T, int Hq) {
+  const int64_t tiles = (static_cast<int64_t>(view(c).cap) + 127) / 128;
+  const int64_t groups = static_cast<int64_t>(c->batch) * c->num_kv_heads;
+  const int64_t rows = static_cast<int64_t>(Hq / c->num_kv_heads) * T;
+  return static_cast<double>(tiles) * groups * ((rows + 15) / 16) >= 2147483648.0 ||
+         static_cast<double>(groups) * rows >= 2147483648.0;
+}
+
 bool tree_shape(const lyc_layer_cache* c, int T, int Hq, bool may_tc, TreeShape* s) {
   const int sms = sm_count(c->device);
   if (sms < 1) return false;
@@ -170,6 +179,7 @@ lyc_status check_tree(const lyc_layer_cache* c, int T, int Hq) {
   if (T < 1 || T > 256) return refuse(LYC_ERR_UNSUPPORTED, "T %d is not in [1, 256]", T);
   if (Hq < c->num_kv_heads || Hq > kMaxHeads || Hq % c->num_kv_heads != 0)
     return refuse(LYC_ERR_INVALID_ARG, "num_q_heads %d is not a multiple of num_kv_heads %d", Hq, c->num_kv_heads);
+  if (tree_too_large(c, T, Hq)) return refuse(LYC_ERR_UNSUPPORTED, "capacity * batch * heads * T is too large");
   return LYC_OK;
 }
 

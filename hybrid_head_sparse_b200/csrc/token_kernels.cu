@@ -18,7 +18,29 @@ namespace lyc {
 
 namespace {
 
-// 16 bytes of bf16 or fp32 as floats.
+// Two fp32 operations an instruction (sm_100's packed forms).
+__device__ __forceinline__ unsigned long long as_u64(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 as_f2(unsigned long long r) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+  return as_f2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+  return as_f2(r);
+}
+
+// 16 or 8 bytes of bf16 or fp32 as floats.
 template <typename T>
 struct Vec;
 template <>
@@ -32,25 +54,33 @@ struct Vec<__nv_bfloat16> {
       f[2 * i + 1] = bf16hi(w[i]);
     }
   }
+  static __device__ __forceinline__ void unpack(const uint2& u, float2* f) {
+    f[0] = make_float2(bf16lo(u.x), bf16hi(u.x));
+    f[1] = make_float2(bf16lo(u.y), bf16hi(u.y));
+  }
+  static __device__ __forceinline__ uint32_t pair(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
   static __device__ __forceinline__ uint4 pack(const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+  }
+  static __device__ __forceinline__ uint2 pack(const float2* f) {
+    return make_uint2(pair(f[0].x, f[0].y), pair(f[1].x, f[1].y));
   }
 };
 template <>
 struct Vec<float> {
   static constexpr int N = 4;
-  static __device__ __forceinline__ void unpack(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x);
-    f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z);
-    f[3] = __uint_as_float(u.w);
+  static __device__ __forceinline__ void unpack(const uint2& u, float2* f) {
+    f[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
   }
   static __device__ __forceinline__ uint4 pack(const float* f) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ uint2 pack(const float2* f) {
+    return make_uint2(__float_as_uint(f[0].x), __float_as_uint(f[0].y));
   }
 };
 
@@ -71,26 +101,29 @@ __device__ __forceinline__ int scale_byte(uint32_t max_bits) {
 }
 
 // ---------------------------------------------------------------- tokens
-// One block per token; LPH lanes hold a head's row, 16 bytes each, so a row's
-// sums are shuffles within the LPH lanes and a rotation's partner elements
-// are either in the lane (adjacent pairs) or in the lane half/N away.  The
-// token's half angles are taken once, in 64 bits: the turn pos * inv_freq /
+// One block per token.  LPH lanes hold a head's row, two 8-byte chunks each:
+// the chunks of rotation partners (elements i and i + rot_dim/2, or adjacent
+// ones) lie in one lane, so a row's only shuffles are those of its sum.  A
+// lane has the same elements of every head, so its turns and weights stay in
+// registers, and fp32 runs two operations an instruction: the first form (a
+// lane with 16 adjacent bytes, partners by shuffle, turns from shared memory)
+// was bound by instructions, 250 a row against about 60.
+//
+// The token's angles are taken once, in 64 bits: the turn pos * inv_freq /
 // 2 pi less its nearest whole number, then sincospi of that in 32 bits
 // (positions reach 2^20, where a 32-bit product is off by up to 2^-4 rad).
-// Heads 0..Hq-1 of the block's list are the queries, then the keys, then the
-// values.
-constexpr int kTokenThreads = 256;
-
 template <typename T, int D, bool APPEND, bool F8>
-__global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ TokenParams p) {
+__global__ void __launch_bounds__(512) token_kernel(const __grid_constant__ TokenParams p) {
   constexpr int N = Vec<T>::N;
+  constexpr int CE = N / 2;   // elements of a chunk
+  constexpr int C2 = CE / 2;  // pairs of a chunk
   constexpr int LPH = D / N;
   constexpr int ES = sizeof(T);
   __shared__ float2 turn[D / 2];
   pdl_wait();
   pdl_launch_dependents();
   const int64_t r = blockIdx.x;
-  const int b = static_cast<int>(r / p.T), t = static_cast<int>(r % p.T);
+  const int b = static_cast<int>(r / p.T), t = static_cast<int>(r - static_cast<int64_t>(b) * p.T);
   int64_t pos = 0;
   RowAt at{0, 0};
   bool stored = true;
@@ -110,7 +143,40 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
     pos = p.pos[r];
     if (pos < 0) return;
   }
-  for (int i = threadIdx.x; i < p.half; i += kTokenThreads) {
+
+  const int lane = threadIdx.x % LPH;  // within the head's row
+  const int slot = threadIdx.x / LPH, slots = blockDim.x / LPH;
+  // the lane's chunks: partners, and past the rotated elements neighbours
+  const int hl = p.interleaved ? 0 : p.half / CE;
+  const int ca = lane < hl ? lane : 2 * lane, cb = lane < hl ? lane + hl : 2 * lane + 1;
+  const bool rot = p.interleaved ? lane * N < 2 * p.half : lane < hl;
+
+  auto load = [&](const unsigned char* row, bool live, float2* x) {
+    uint2 ua = make_uint2(0u, 0u), ub = ua;
+    if (live) {
+      ua = *reinterpret_cast<const uint2*>(row + ca * 8);
+      ub = *reinterpret_cast<const uint2*>(row + cb * 8);
+    }
+    Vec<T>::unpack(ua, x);
+    Vec<T>::unpack(ub, x + C2);
+  };
+  auto fetch = [&](const unsigned char* row, bool live, uint2* u) {
+    u[0] = u[1] = make_uint2(0u, 0u);
+    if (live) {
+      u[0] = *reinterpret_cast<const uint2*>(row + ca * 8);
+      u[1] = *reinterpret_cast<const uint2*>(row + cb * 8);
+    }
+  };
+  const unsigned char* qrow = p.q + (b * p.q_batch + t * p.q_token) * ES;
+  const unsigned char* krow = p.k + (b * p.k_batch + t * p.k_token) * ES;
+  const unsigned char* vrow = p.v + (b * p.v_batch + t * p.v_token) * ES;
+  // asked for before the angles: the block's first rows
+  uint2 uq[2], uk[2], uv[2];
+  fetch(qrow + slot * p.q_head * ES, slot < p.Hq, uq);
+  fetch(krow + slot * p.k_head * ES, slot < p.Hk, uk);
+  if (APPEND) fetch(vrow + slot * p.v_head * ES, slot < p.Hv, uv);
+
+  for (int i = threadIdx.x; i < p.half; i += blockDim.x) {
     double x = static_cast<double>(pos) * static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;  // 1 / (2 pi)
     x -= rint(x);
     float s, c;
@@ -118,98 +184,125 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_const
     turn[i] = make_float2(c, s);
   }
   __syncthreads();
+  // cosines and sines of the lane's pairs: [j] of elements 2j, 2j+1 of both
+  // chunks (partners), or of each chunk's pairs in turn (adjacent)
+  float2 cs[C2], sn[C2], ns[C2];
+  if (rot && !p.interleaved) {
+#pragma unroll
+    for (int j = 0; j < C2; ++j) {
+      const float2 u = turn[lane * CE + 2 * j], v = turn[lane * CE + 2 * j + 1];
+      cs[j] = make_float2(u.x, v.x);
+      sn[j] = make_float2(u.y, v.y);
+      ns[j] = make_float2(-u.y, -v.y);
+    }
+  }
 
-  const int lane = threadIdx.x % LPH;  // within the head's row
-  const int total = p.Hq + p.Hk + p.Hv;
-  // every lane of a warp takes part in the shuffles: whole warps go around
-  const int rounds = (total * LPH + kTokenThreads - 1) / kTokenThreads;
-  for (int it = 0; it < rounds; ++it) {
-    const int h = (it * kTokenThreads + static_cast<int>(threadIdx.x)) / LPH;
-    const bool isq = h < p.Hq, isk = !isq && h < p.Hq + p.Hk;
-    const bool live = h < total && (isq || !APPEND || stored);
-    const int hh = isq ? h : isk ? h - p.Hq : h - p.Hq - p.Hk;
-    float x[N];
+  // norm (w != NULL) and rotation of one row; whole warps
+  auto turned = [&](float2* x, bool norm, const float2* w) {
+    if (norm) {
+      float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = 0.f;
-    if (live) {
-      const unsigned char* src = isq   ? p.q + (b * p.q_batch + t * p.q_token + hh * p.q_head) * ES
-                                 : isk ? p.k + (b * p.k_batch + t * p.k_token + hh * p.k_head) * ES
-                                       : p.v + (b * p.v_batch + t * p.v_token + hh * p.v_head) * ES;
-      Vec<T>::unpack(*reinterpret_cast<const uint4*>(src + lane * 16), x);
-    }
-    const unsigned char* w = isq ? p.q_weight : isk ? p.k_weight : nullptr;
-    float ss = 0.f;
+      for (int j = 0; j < 2 * C2; ++j) a = fma2(x[j], x[j], a);
+      float ss = a.x + a.y;
 #pragma unroll
-    for (int j = 0; j < N; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (w) {
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-      float g[N];
-      Vec<T>::unpack(*reinterpret_cast<const uint4*>(w + lane * 16), g);
+      const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-      for (int j = 0; j < N; ++j) x[j] = x[j] * inv * g[j];
+      for (int j = 0; j < 2 * C2; ++j) x[j] = mul2(mul2(x[j], inv2), w[j]);
     }
-    if (p.half > 0) {
-      if (p.interleaved) {
-        if ((isq || isk) && lane * N < 2 * p.half) {
+    if (rot) {
+      if (!p.interleaved) {
 #pragma unroll
-          for (int j = 0; j < N; j += 2) {
-            const float2 cs = turn[lane * (N / 2) + j / 2];
-            const float a = x[j], c = x[j + 1];
-            x[j] = a * cs.x - c * cs.y;
-            x[j + 1] = c * cs.x + a * cs.y;
-          }
+        for (int j = 0; j < C2; ++j) {
+          const float2 u = x[j], v = x[j + C2];
+          x[j] = fma2(v, ns[j], mul2(u, cs[j]));
+          x[j + C2] = fma2(u, sn[j], mul2(v, cs[j]));
         }
       } else {
-        const int hl = p.half / N;  // lanes of the first elements of the pairs
-        const bool lo = lane < hl, rot = (isq || isk) && lane < 2 * hl;
-        const int base = static_cast<int>(threadIdx.x & 31) - lane;
-        const int from = rot ? base + (lo ? lane + hl : lane - hl) : base + lane;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float other = __shfl_sync(0xffffffffu, x[j], from);
-          if (rot) {
-            const float2 cs = turn[(lo ? lane : lane - hl) * N + j];
-            x[j] = lo ? x[j] * cs.x - other * cs.y : x[j] * cs.x + other * cs.y;
-          }
+        for (int j = 0; j < 2 * C2; ++j) {
+          const float2 cv = turn[lane * (N / 2) + j];
+          x[j] = make_float2(x[j].x * cv.x - x[j].y * cv.y, x[j].y * cv.x + x[j].x * cv.y);
         }
       }
     }
-    uint32_t mx = 0;
-    if (APPEND && F8) {  // magnitudes as integers: a NaN is above every number
-#pragma unroll
-      for (int j = 0; j < N; ++j) mx = max(mx, __float_as_uint(x[j]) & 0x7fffffffu);
-#pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  };
+  auto store = [&](unsigned char* row, const float2* x) {
+    *reinterpret_cast<uint2*>(row + ca * 8) = Vec<T>::pack(x);
+    *reinterpret_cast<uint2*>(row + cb * 8) = Vec<T>::pack(x + C2);
+  };
+  // one row into the cache
+  auto keep = [&](unsigned char* rows, unsigned char* scales, int h, bool live, const float2* x) {
+    if (!F8) {
+      if (live) store(rows + (at.kv + h * p.cache.s_head) * ES, x);
+      return;
     }
-    if (!live) continue;
-    if (isq) {
-      *reinterpret_cast<uint4*>(p.q_out + (b * p.qo_batch + t * p.qo_token + hh * p.qo_head) * ES + lane * 16) =
-          Vec<T>::pack(x);
-    } else if (!APPEND) {
-      *reinterpret_cast<uint4*>(p.k_out + (b * p.ko_batch + t * p.ko_token + hh * p.ko_head) * ES + lane * 16) =
-          Vec<T>::pack(x);
-    } else if (!F8) {
-      unsigned char* dst = (isk ? p.cache.k : p.cache.v) + (at.kv + hh * p.cache.s_head) * ES;
-      *reinterpret_cast<uint4*>(dst + lane * 16) = Vec<T>::pack(x);
-    } else {
-      const int e = scale_byte(mx);
-      // 2^-(e - 127); a row that is not finite gets zero codes
-      const float inv = e == 255 ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-      uint32_t c[N / 4];
+    uint32_t mx = 0;  // magnitudes as integers: a NaN is above every number
 #pragma unroll
-      for (int j = 0; j < N / 4; ++j)
-        c[j] = e4m3x2(x[4 * j] * inv, x[4 * j + 1] * inv) | (e4m3x2(x[4 * j + 2] * inv, x[4 * j + 3] * inv) << 16);
-      if (e == 255)
+    for (int j = 0; j < 2 * C2; ++j)
+      mx = max(mx, max(__float_as_uint(x[j].x) & 0x7fffffffu, __float_as_uint(x[j].y) & 0x7fffffffu));
 #pragma unroll
-        for (int j = 0; j < N / 4; ++j) c[j] = 0u;
-      unsigned char* dst = (isk ? p.cache.k : p.cache.v) + at.kv + hh * p.cache.s_head + lane * N;
-      if (N == 8)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(c[0], c[N / 4 - 1]);
-      else
-        *reinterpret_cast<uint32_t*>(dst) = c[0];
-      if (lane == 0) (isk ? p.cache.ks : p.cache.vs)[at.sc + hh * p.cache.ss_head] = static_cast<unsigned char>(e);
+    for (int o = LPH / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (!live) return;
+    const int e = scale_byte(mx);
+    const float inv = __uint_as_float(static_cast<uint32_t>(max(254 - e, 0)) << 23);  // 2^-(e - 127)
+    unsigned char* dst = rows + at.kv + h * p.cache.s_head;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float2* y = x + c * C2;
+      uint32_t code = 0u;  // a row that is not finite gets zero codes
+      if (e != 255) code = e4m3x2(y[0].x * inv, y[0].y * inv);
+      if (C2 == 2 && e != 255) code |= e4m3x2(y[C2 - 1].x * inv, y[C2 - 1].y * inv) << 16;
+      *reinterpret_cast<uint32_t*>(dst + (c ? cb : ca) * 4) = code;
+    }
+    if (lane == 0) scales[at.sc + h * p.cache.ss_head] = static_cast<unsigned char>(e);
+  };
+
+  const int qrounds = (p.Hq + slots - 1) / slots;
+  if (qrounds > 0) {
+    float2 w[2 * C2];
+    const bool norm = p.q_weight != nullptr;
+    load(p.q_weight, norm, w);
+    unsigned char* out = p.q_out + (b * p.qo_batch + t * p.qo_token) * ES;
+    for (int it = 0; it < qrounds; ++it) {
+      const int h = it * slots + slot, next = h + slots;
+      float2 x[2 * C2];
+      Vec<T>::unpack(uq[0], x);
+      Vec<T>::unpack(uq[1], x + C2);
+      fetch(qrow + next * p.q_head * ES, next < p.Hq, uq);
+      turned(x, norm, w);
+      if (h < p.Hq) store(out + h * p.qo_head * ES, x);
+    }
+  }
+  const int krounds = (p.Hk + slots - 1) / slots;
+  if (krounds > 0) {
+    float2 w[2 * C2];
+    const bool norm = p.k_weight != nullptr;
+    load(p.k_weight, norm, w);
+    unsigned char* out = p.k_out + (b * p.ko_batch + t * p.ko_token) * ES;
+    for (int it = 0; it < krounds; ++it) {
+      const int h = it * slots + slot, next = h + slots;
+      float2 x[2 * C2];
+      Vec<T>::unpack(uk[0], x);
+      Vec<T>::unpack(uk[1], x + C2);
+      fetch(krow + next * p.k_head * ES, next < p.Hk, uk);
+      turned(x, norm, w);
+      if (APPEND)
+        keep(p.cache.k, p.cache.ks, h, h < p.Hk && stored, x);
+      else if (h < p.Hk)
+        store(out + h * p.ko_head * ES, x);
+    }
+  }
+  if (APPEND) {
+    const int vrounds = (p.Hv + slots - 1) / slots;
+    for (int it = 0; it < vrounds; ++it) {
+      const int h = it * slots + slot, next = h + slots;
+      float2 x[2 * C2];
+      Vec<T>::unpack(uv[0], x);
+      Vec<T>::unpack(uv[1], x + C2);
+      fetch(vrow + next * p.v_head * ES, next < p.Hv, uv);
+      keep(p.cache.v, p.cache.vs, h, h < p.Hv && stored, x);
     }
   }
 }
@@ -323,9 +416,20 @@ cudaError_t launch_pdl(K kernel, const P& p, unsigned grid, int threads, cudaStr
 
 }  // namespace
 
+// Threads of a token's block.  Few tokens: enough for all its heads at once, the
+// call is a chain of latencies.  Many: 128, so that the block's start (the
+// position, the angles) is shared by fewer warps.
+static int token_threads(const TokenParams* p, int head_dim, int dtype) {
+  if (p->rows > 1024) return 128;
+  const int lanes = head_dim / (dtype == LYC_BF16 ? 8 : 4);
+  const int want = (p->Hq > p->Hk ? p->Hq : p->Hk) * lanes;
+  return want <= 128 ? 128 : want <= 256 ? 256 : 512;
+}
+
 cudaError_t token_launch(const TokenParams* p, int head_dim, int dtype, bool append, int cache_type,
                          cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(p->rows);
+  const int kTokenThreads = token_threads(p, head_dim, dtype);
   const bool f8 = cache_type == LYC_CACHE_E4M3;
   if (append) {
     if (head_dim == 128)

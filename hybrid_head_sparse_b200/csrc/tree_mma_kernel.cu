@@ -28,6 +28,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "lyc_device.cuh"
 #include "serve_plan.h"
@@ -130,19 +131,13 @@ __device__ __forceinline__ uint32_t codes02(uint32_t w) { return codes13(w << 8)
 
 __device__ __forceinline__ uint16_t bf16_bits(const unsigned char* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
-// A piece of work: tiles [t0, t1) of group (b, g, mb).
-struct TmPiece {
-  int b, g, mb, t0, t1;
-  TreeElem e;
-};
-
 // The loads of one warp's chunks: where each row lies is looked up one chunk
 // ahead of its copies, its scale bytes are kept in registers for one chunk
 // before they go to shared memory.
 template <class C>
 struct TmLoader {
   const TreeParams& p;
-  const TmPiece& pc;
+  const TreePiece& pc;
   unsigned char* ring;
   float* scales;
   unsigned long long* okw;
@@ -152,7 +147,7 @@ struct TmLoader {
   int kb[C::KPL], vb[C::KPL];  // scale bytes waiting for shared memory
   int pending;                 // their stage, or -1
 
-  __device__ __forceinline__ TmLoader(const TreeParams& prm, const TmPiece& piece, unsigned char* smem, int w, int l)
+  __device__ __forceinline__ TmLoader(const TreeParams& prm, const TreePiece& piece, unsigned char* smem, int w, int l)
       : p(prm), pc(piece), ring(smem + w * C::WARPB),
         scales(reinterpret_cast<float*>(smem + C::OFF_SC + w * C::ST * C::SCB)),
         okw(reinterpret_cast<unsigned long long*>(smem + C::OFF_OK) + w * C::ST), warp(w), lane(l),
@@ -245,27 +240,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
       tree_elem(p, b, &bad);
       if (bad) atomicOr(p.status, LYC_OP_BAD_LENGTH);
     }
-  const TreeSched<C::TR, C::ROWS> sched(p);
+  TreeWalk<C::TR, C::ROWS> walk(p);
   const int cta = blockIdx.x;
-  const int64_t xbeg = sched.begin(cta), xend = sched.begin(cta + 1);
   const float NEG = -INFINITY;
+  TreePiece pc;
 
-  for (int64_t x = xbeg; x < xend;) {
-    TmPiece pc;
-    int64_t efirst;
-    sched.locate(x, &pc.b, &efirst);
-    bool bad = false;
-    pc.e = tree_elem(p, pc.b, &bad);
-    const int nt = (pc.e.n + C::TR - 1) / C::TR;
-    const int64_t rel = x - efirst;
-    const int grp = static_cast<int>(rel / nt);
-    const int mbs = sched.blocks(pc.e);
-    pc.g = grp / mbs;
-    pc.mb = grp % mbs;
-    pc.t0 = static_cast<int>(rel - static_cast<int64_t>(grp) * nt);
-    pc.t1 = static_cast<int>(min(static_cast<int64_t>(nt), pc.t0 + (xend - x)));
-    x += pc.t1 - pc.t0;
-
+  while (walk.next(&pc)) {
     const int first_draft = pc.e.n - pc.e.cnt;
     TmLoader<C> ld(p, pc, smem, warp, lane);
     ld.look_up(0);
@@ -561,7 +541,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
     }
     cp_wait<0>();
 
-    // merge the eight warps' states; each warp's output goes into its ring
+    // merge the eight warps' states of the rows that are queries; each warp's
+    // output goes into its ring
+    const int rows = min(C::ROWS, pc.e.cnt * p.G - pc.mb * C::ROWS);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     float* ow = reinterpret_cast<float*>(ld.ring);
     __syncwarp();
@@ -569,11 +551,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
+        if (mt * 16 + hf * 8 >= rows) continue;
         const int row = mt * 16 + hf * 8 + g4;
         float ls = l[mt][hf];
         ls += __shfl_xor_sync(FULL, ls, 1);
         ls += __shfl_xor_sync(FULL, ls, 2);
         if (j4 == 0) ml[warp * C::ROWS + row] = make_float2(m[mt][hf], ls);
+        if (row >= rows) continue;
         if (!C::F8) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -589,40 +573,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
         }
       }
     __syncthreads();
-    {
-      constexpr int TPR = C::THREADS / C::ROWS, DPT = D / TPR;
-      const int row = threadIdx.x / TPR, d0 = (threadIdx.x % TPR) * DPT;
-      float M = NEG, L = 0.f, acc[DPT];
+    for (int x = threadIdx.x; x < rows * (D / 4); x += C::THREADS) {
+      const int row = x / (D / 4), d0 = x % (D / 4) * 4;
+      float M = NEG, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < C::NW; ++w) M = fmaxf(M, ml[w * C::ROWS + row].x);
-#pragma unroll
-      for (int k = 0; k < DPT; ++k) acc[k] = 0.f;
 #pragma unroll
       for (int w = 0; w < C::NW; ++w) {
         const float2 s = ml[w * C::ROWS + row];
         const float f = s.x == NEG ? 1.f : ex2(s.x - M);  // 1: the state is zero, or NaN
         L = fmaf(s.y, f, L);
-        const float* src = reinterpret_cast<const float*>(smem + w * C::WARPB) + row * D + d0;
-#pragma unroll
-        for (int k = 0; k < DPT; ++k) acc[k] = fmaf(src[k], f, acc[k]);
+        const float4 u = *reinterpret_cast<const float4*>(smem + w * C::WARPB + (row * D + d0) * 4);
+        acc.x = fmaf(u.x, f, acc.x);
+        acc.y = fmaf(u.y, f, acc.y);
+        acc.z = fmaf(u.z, f, acc.z);
+        acc.w = fmaf(u.w, f, acc.w);
       }
       const int i = pc.mb * C::ROWS + row;
       const int t = i / p.G, h = pc.g * p.G + i % p.G;
-      if (t < pc.e.cnt) {
-        if (pc.t0 == 0 && pc.t1 == nt) {
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          unsigned char* dst = p.out + 2 * (pc.b * p.o_batch + t * p.o_token + h * p.o_head + d0);
-#pragma unroll
-          for (int k = 0; k < DPT; k += 2)
-            reinterpret_cast<uint32_t*>(dst)[k / 2] = pack16<false>(acc[k] * inv, acc[k + 1] * inv);
-        } else {
-          const int64_t slot = 2 * static_cast<int64_t>(cta) + (pc.t0 == 0 ? 1 : 0);
-          float* dst = p.part_o + (slot * C::ROWS + row) * D + d0;
-#pragma unroll
-          for (int k = 0; k < DPT; k += 4)
-            *reinterpret_cast<float4*>(dst + k) = make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]);
-          if (d0 == 0) p.part_ml[slot * C::ROWS + row] = make_float2(M, L);
-        }
+      if (pc.t0 == 0 && pc.t1 == pc.nt) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        *reinterpret_cast<uint2*>(p.out + 2 * (pc.b * p.o_batch + t * p.o_token + h * p.o_head + d0)) =
+            make_uint2(pack16<false>(acc.x * inv, acc.y * inv), pack16<false>(acc.z * inv, acc.w * inv));
+      } else {
+        const int64_t slot = 2 * static_cast<int64_t>(cta) + (pc.t0 == 0 ? 1 : 0);
+        *reinterpret_cast<float4*>(p.part_o + (slot * C::ROWS + row) * D + d0) = acc;
+        if (d0 == 0) p.part_ml[slot * C::ROWS + row] = make_float2(M, L);
       }
     }
     __syncthreads();
@@ -630,57 +607,77 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
 }
 
 // One warp for each query row of each group: merges the states of the CTAs
-// among which the group was cut, in their order.
+// among which the group was cut, in their order.  The lengths are inputs of
+// the whole call, complete before the attention kernel lets this one start,
+// so the division of work is computed while that one runs; then the rows of
+// up to kParts parts and their (m, l) are asked for at once, and what is left
+// is one trip to L2 (part after part it was 5.6 us of a 17 us call).
+constexpr int kParts = 20;
+
 template <int D, int ROWS, int TR>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeParams p) {
   const int lane = threadIdx.x & 31;
-  pdl_wait();
-  const TreeSched<TR, ROWS> sched(p);
-  if (sched.total == 0) return;
-  const int rows = p.G * p.T;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int i = static_cast<int>(w % rows);
-  const int64_t bg = w / rows;
-  const int g = static_cast<int>(bg % p.Hkv);
-  const int64_t b = bg / p.Hkv;
-  if (b >= p.B) return;
-  bool bad = false;
-  const TreeElem e = tree_elem(p, static_cast<int>(b), &bad);
+  const uint32_t rows = static_cast<uint32_t>(p.G) * p.T;
+  const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const uint32_t bg = w / rows;
+  const int i = static_cast<int>(w - bg * rows);
+  const int b = static_cast<int>(bg / p.Hkv);
+  const int g = static_cast<int>(bg) - b * p.Hkv;
   const int t = i / p.G, h = g * p.G + i % p.G;
-  if (t >= e.cnt) return;
+  const TreeSched<TR, ROWS> sched(p);
+  const TreeElem e = b < p.B ? sched.elem(b) : TreeElem{0, 0};
   const int mb = i / ROWS, row = i % ROWS;
-  const int nt = (e.n + TR - 1) / TR;
-  const int64_t x0 = sched.first_tile(static_cast<int>(b)) + static_cast<int64_t>(g * sched.blocks(e) + mb) * nt;
-  const int c0 = sched.owner(x0), c1 = sched.owner(x0 + nt - 1);
-  if (c0 == c1) return;  // its CTA wrote the output
+  const uint32_t nt = static_cast<uint32_t>((e.n + TR - 1) / TR);
+  int c0 = 0, c1 = 0;
+  if (t < e.cnt) {
+    const uint32_t x0 = sched.first_tile(b) + static_cast<uint32_t>(g * sched.blocks(e) + mb) * nt;
+    c0 = static_cast<int>(sched.owner(x0));
+    c1 = static_cast<int>(sched.owner(x0 + nt - 1));
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (c0 == c1) return;  // nothing to do, or its CTA wrote the output
   constexpr int V = D / 32;
-  auto slot_of = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * ROWS + row; };
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[slot_of(c)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[V];
+  typedef typename std::conditional<V == 4, float4, float2>::type Part;
+  const int parts = c1 - c0 + 1;
+  const float NEG = -INFINITY;
+  float M = NEG, L = 0.f, acc[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) acc[k] = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int64_t s = slot_of(c);
-    const float2 ml = p.part_ml[s];
-    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - M);  // 1: the state is zero, or NaN
-    L = fmaf(ml.y, f, L);
-    const float* src = p.part_o + s * D + lane * V;
-    if (V == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(u.x, f, acc[0]);
-      acc[1] = fmaf(u.y, f, acc[1]);
-      acc[V - 2] = fmaf(u.z, f, acc[V - 2]);
-      acc[V - 1] = fmaf(u.w, f, acc[V - 1]);
-    } else {
-      const float2 u = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(u.x, f, acc[0]);
-      acc[1] = fmaf(u.y, f, acc[1]);
+  for (int k0 = 0; k0 < parts; k0 += kParts) {
+    const int64_t s0 = 2 * static_cast<int64_t>(c0 + k0) * ROWS + row;
+    Part u[kParts];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      // a group's first part lies in its CTA's second slot
+      const int64_t s = s0 + (2 * k + (k0 + k == 0 ? 1 : 0)) * static_cast<int64_t>(ROWS);
+      if (k0 + k < parts) u[k] = *reinterpret_cast<const Part*>(p.part_o + s * D + lane * V);
+    }
+    float2 ml = make_float2(NEG, 0.f);
+    if (lane < kParts && k0 + lane < parts)
+      ml = p.part_ml[s0 + (2 * lane + (k0 + lane == 0 ? 1 : 0)) * static_cast<int64_t>(ROWS)];
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float top = fmaxf(M, m);
+    const float keep = M == NEG ? 1.f : ex2(M - top);  // 1: the state is zero, or NaN
+    const float f = ml.x == NEG ? 1.f : ex2(ml.x - top);
+    M = top;
+    L = fmaf(L, keep, ml.y * f);  // lane j sums parts j, j + kParts, ...
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] *= keep;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      if (k0 + k < parts) {
+        const float* v = reinterpret_cast<const float*>(&u[k]);
+#pragma unroll
+        for (int c = 0; c < V; ++c) acc[c] = fmaf(v[c], fk, acc[c]);
+      }
     }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   const float inv = L == 0.f ? 0.f : 1.f / L;
   unsigned char* dst = p.out + 2 * (b * p.o_batch + t * p.o_token + h * p.o_head + lane * V);
 #pragma unroll
@@ -714,8 +711,8 @@ template <int D, int ROWS, int TR>
 cudaError_t launch_combine(const TreeParams* p, cudaStream_t stream) {
   const int64_t warps = static_cast<int64_t>(p->B) * p->Hkv * p->G * p->T;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -214,39 +214,7 @@ __host__ __device__ constexpr uint32_t idesc128(uint32_t type, int b_mn_major) {
          ((128u >> 4) << 24);
 }
 
-struct TcPiece {
-  int b, g, mb, t0, t1, nt;
-  TreeElem e;
-};
-
-// The CTA's pieces in order; every warp walks them for itself.
-template <class C>
-struct TcWalk {
-  const TreeParams& p;
-  TreeSched<kRows, kRows> sched;
-  int64_t x, xend;
-  __device__ __forceinline__ explicit TcWalk(const TreeParams& prm) : p(prm), sched(prm) {
-    x = sched.begin(blockIdx.x);
-    xend = sched.begin(blockIdx.x + 1);
-  }
-  __device__ __forceinline__ bool next(TcPiece* pc) {
-    if (x >= xend) return false;
-    int64_t first;
-    sched.locate(x, &pc->b, &first);
-    bool bad = false;
-    pc->e = tree_elem(p, pc->b, &bad);
-    pc->nt = (pc->e.n + kRows - 1) / kRows;
-    const int64_t rel = x - first;
-    const int grp = static_cast<int>(rel / pc->nt);
-    const int mbs = sched.blocks(pc->e);
-    pc->g = grp / mbs;
-    pc->mb = grp % mbs;
-    pc->t0 = static_cast<int>(rel - static_cast<int64_t>(grp) * pc->nt);
-    pc->t1 = static_cast<int>(min(static_cast<int64_t>(pc->nt), pc->t0 + (xend - x)));
-    x += pc->t1 - pc->t0;
-    return true;
-  }
-};
+typedef TreeWalk<kRows, kRows> TcWalk;
 
 // ---------------------------------------------------------------- loads
 // The whole warp: lane j looks up and copies box j of a tile (one box of 128
@@ -262,8 +230,8 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
   const bool paged = p.cache.bt != nullptr;
   const int nbox = kRows / P.t.box_rows;
   const uint32_t boxb = static_cast<uint32_t>(C::TILEB) / nbox;  // bytes of a box
-  TcWalk<C> walk(p);
-  TcPiece pc;
+  TcWalk walk(p);
+  TreePiece pc;
   int t = 0;
   int asked[2] = {0, 0};  // tiles of K and of V whose copies went out
   bool ok = true;
@@ -334,8 +302,8 @@ __device__ __forceinline__ void tc_mma(const TreeTcParams& P, unsigned char* sme
   const uint32_t qbase = smem_u32(smem + C::OFF_Q);
   const uint32_t kbase = smem_u32(smem + C::OFF_K);
   const uint32_t vbase = smem_u32(smem + (C::F8 ? C::OFF_VC : C::OFF_V));
-  TcWalk<C> walk(p);
-  TcPiece pc;
+  TcWalk walk(p);
+  TreePiece pc;
   int t = 0, piece = 0;
   bool ok = true;
 
@@ -422,8 +390,8 @@ __device__ __forceinline__ void tc_convert(const TreeTcParams& P, unsigned char*
   TcBars<C> br(smem);
   const TcShared sh = shared_of<C>(smem);
   float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE);
-  TcWalk<C> walk(p), ahead(p);
-  TcPiece pc, apc;
+  TcWalk walk(p), ahead(p);
+  TreePiece pc, apc;
   int at = 0;  // the next tile of apc whose scales are read
   bool amore = ahead.next(&apc);
   if (amore) at = apc.t0;
@@ -503,7 +471,7 @@ __device__ __forceinline__ void tc_convert(const TreeTcParams& P, unsigned char*
 
 // ---------------------------------------------------------------- softmax warps
 // Bits x of the result: row kb + x (x < 64) is seen by node t.
-__device__ __forceinline__ unsigned long long seen_bits(const TreeParams& p, const TcPiece& pc, int t, int kb,
+__device__ __forceinline__ unsigned long long seen_bits(const TreeParams& p, const TreePiece& pc, int t, int kb,
                                                         uint32_t okbox, int box_rows) {
   const int first = pc.e.n - pc.e.cnt;
   const int node0 = kb - first;  // node of bit 0 (negative: rows before the draft)
@@ -555,8 +523,8 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
   auto ml_of = [&](int x) {
     return reinterpret_cast<float2*>(qbuf + (C::F8 ? i * 128 + (((x * 4) ^ (i & 7)) << 4) : tile_off(i, x * 8)));
   };
-  TcWalk<C> walk(p);
-  TcPiece pc;
+  TcWalk walk(p);
+  TreePiece pc;
   int t = 0, piece = 0;
   while (walk.next(&pc)) {
     const int row = pc.mb * kRows + i;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -186,11 +187,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.lyc_destroy.restype = None
     L.lyc_sparse_attention_noalloc.argtypes = [P, ctypes.POINTER(lyc_kv_cache), I, I, I, I, P, I,
                                                P, P, P]
-    L.lyc_qk_norm_rope.argtypes = [ctypes.POINTER(lyc_rope_args), P]
-    L.lyc_cache_append.argtypes = [ctypes.POINTER(lyc_layer_cache), ctypes.POINTER(lyc_append_args), P]
-    L.lyc_cache_read.argtypes = [ctypes.POINTER(lyc_layer_cache), ctypes.POINTER(lyc_read_args), P]
+    L.lyc_qk_norm_rope.argtypes = [P, P]
+    L.lyc_cache_append.argtypes = [ctypes.POINTER(lyc_layer_cache), P, P]
+    L.lyc_cache_read.argtypes = [ctypes.POINTER(lyc_layer_cache), P, P]
     L.lyc_tree_workspace_bytes.argtypes = [ctypes.POINTER(lyc_layer_cache), I, I]
-    L.lyc_tree_attention.argtypes = [ctypes.POINTER(lyc_layer_cache), ctypes.POINTER(lyc_tree_args), P]
+    L.lyc_tree_attention.argtypes = [ctypes.POINTER(lyc_layer_cache), P, P]
     for name in EXPORTED:
         if name not in ("lyc_status_string", "lyc_last_error", "lyc_destroy"):
             getattr(L, name).restype = I
@@ -306,15 +307,15 @@ def lyc_destroy(ctx) -> None:
 
 
 def lyc_qk_norm_rope(args: lyc_rope_args, stream) -> int:
-    return load().lyc_qk_norm_rope(args, stream)
+    return load().lyc_qk_norm_rope(ctypes.byref(args), stream)
 
 
 def lyc_cache_append(cache: lyc_layer_cache, args: lyc_append_args, stream) -> int:
-    return load().lyc_cache_append(cache, args, stream)
+    return load().lyc_cache_append(cache, ctypes.byref(args), stream)
 
 
 def lyc_cache_read(cache: lyc_layer_cache, args: lyc_read_args, stream) -> int:
-    return load().lyc_cache_read(cache, args, stream)
+    return load().lyc_cache_read(cache, ctypes.byref(args), stream)
 
 
 def lyc_tree_workspace_bytes(cache: lyc_layer_cache, T: int, num_q_heads: int) -> int:
@@ -323,7 +324,7 @@ def lyc_tree_workspace_bytes(cache: lyc_layer_cache, T: int, num_q_heads: int) -
 
 
 def lyc_tree_attention(cache: lyc_layer_cache, args: lyc_tree_args, stream) -> int:
-    return load().lyc_tree_attention(cache, args, stream)
+    return load().lyc_tree_attention(cache, ctypes.byref(args), stream)
 
 
 def lyc_operator_error() -> str:
@@ -522,47 +523,51 @@ def _operator_check(rc: int, where: str):
         raise LycError(rc, where, lyc_operator_error())
 
 
-def _same_device(where, index, **tensors):
-    for name, t in tensors.items():
-        if t is not None and (t.device.type != "cuda" or t.device.index != index):
-            _refuse(where, f"{name} is on {t.device}, not on cuda:{index}")
+# The argument structs are packed by `struct` in the C compiler's layout: a
+# small call's host time is a good part of it, and filling a ctypes.Structure
+# of some thirty fields takes about three times as long.
+_ROPE_ARGS = struct.Struct("@4P8q4Pq5if2i")
+_APPEND_ARGS = struct.Struct("@4P12q6P4ifP")
+_READ_ARGS = struct.Struct("@2P3q2Pq3iP")
+_TREE_ARGS = struct.Struct("@2P6q3P2ifPQP")
 
 
-def _typed(where, name, t, dtype, shape):
-    if t.dtype != dtype:
-        _refuse(where, f"{name} is {t.dtype}, not {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        _refuse(where, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+def _operators():
+    return _lib if _lib is not None else load()
 
 
-def _packed(where, name, t, dtype, shape):
-    _typed(where, name, t, dtype, shape)
-    if not t.is_contiguous():
-        _refuse(where, f"{name} must be contiguous")
+def _rows_in(where, name, t, dtype, shape, index):
+    """(address, strides) of a tensor whose rows (last dimension) are contiguous."""
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or st[-1] != 1:
+        _refuse(where, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device} with strides {st}, where {dtype} "
+                       f"{tuple(shape)} on cuda:{index} with contiguous rows is needed")
+    return t.data_ptr(), st
 
 
-def _rows_in(where, name, t, dtype, shape):
-    _typed(where, name, t, dtype, shape)
-    if t.stride(-1) != 1:
-        _refuse(where, f"{name}: the elements of a row must be contiguous")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _packed(where, name, t, dtype, shape, index):
+    """Address of a contiguous tensor, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(where, f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, where a contiguous {dtype} "
+                       f"{tuple(shape)} on cuda:{index} is needed")
+    return t.data_ptr()
 
 
 def _stream_on(index: int, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    if stream is None:
-        return torch.cuda.current_stream(index).cuda_stream
-    return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the same pointer without a Stream object
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
 
 
 def _status_ptr(where, status, index):
     import torch
     if status is None:
-        return None
-    if status.dtype not in (torch.int32, torch.uint32) or status.numel() != 1 or status.device.index != index:
+        return 0
+    if status.dtype not in (torch.int32, torch.uint32) or status.numel() != 1 or status.get_device() != index:
         _refuse(where, f"status must be one int32 or uint32 on cuda:{index}")
     return status.data_ptr()
 
@@ -584,43 +589,42 @@ class KvCache:
         where = "KvCache"
         if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
             _refuse(where, "k must be a 4-D bf16 or float8_e4m3fn tensor")
-        if k.device.type != "cuda":
+        if not k.is_cuda:
             _refuse(where, f"k is on {k.device}: the cache lies on a GPU")
-        _rows_in(where, "k", k, k.dtype, k.shape)
-        _rows_in(where, "v", v, k.dtype, k.shape)
-        if k.stride() != v.stride():
+        index = self.device_index = k.get_device()
+        kp, st = _rows_in(where, "k", k, k.dtype, k.shape, index)
+        vp, sv = _rows_in(where, "v", v, k.dtype, k.shape, index)
+        if st != sv:
             _refuse(where, "k and v must have the same strides")
         self.e4m3 = k.dtype == torch.float8_e4m3fn
-        self.device_index = k.device.index
-        _same_device(where, self.device_index, v=v, k_scale=k_scale, v_scale=v_scale, block_table=block_table)
         if (k_scale is None) == self.e4m3 or (v_scale is None) == self.e4m3:
             _refuse(where, "a float8_e4m3fn cache has scales, a bf16 cache has none")
-        ss = (0, 0, 0)
+        ss, ksp, vsp = (0, 0, 0), None, None
         if self.e4m3:
             for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-                if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or t.shape != k.shape[:3]:
-                    _refuse(where, f"{name} must be float8_e8m0fnu or uint8 of shape {tuple(k.shape[:3])}")
+                if t.dtype not in (torch.uint8, torch.float8_e8m0fnu) or t.shape != k.shape[:3] or t.get_device() != index:
+                    _refuse(where, f"{name} must be float8_e8m0fnu or uint8 of shape {tuple(k.shape[:3])} on cuda:{index}")
             if k_scale.stride() != v_scale.stride():
                 _refuse(where, "k_scale and v_scale must have the same strides")
-            ss = k_scale.stride()
-        st = k.stride()
+            ss, ksp, vsp = k_scale.stride(), k_scale.data_ptr(), v_scale.data_ptr()
         self.tensors = (k, v, k_scale, v_scale, block_table)
         kind = LYC_CACHE_E4M3 if self.e4m3 else LYC_CACHE_BF16
         if block_table is None:
             self.batch, self.heads, rows, self.d = k.shape
             self.desc = lyc_layer_cache(
-                k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), st[0], st[1], st[2], 0, ss[0], ss[1], ss[2], 0,
-                None, rows, 0, 0, 0, kind, self.batch, self.heads, self.d, self.device_index)
+                kp, vp, ksp, vsp, st[0], st[1], st[2], 0, ss[0], ss[1], ss[2], 0,
+                None, rows, 0, 0, 0, kind, self.batch, self.heads, self.d, index)
         else:
             pages, page_rows, self.heads, self.d = k.shape
             if block_table.dim() != 2:
                 _refuse(where, "block_table must be [B][max_blocks]")
-            _packed(where, "block_table", block_table, torch.int32, block_table.shape)
+            bt = _packed(where, "block_table", block_table, torch.int32, block_table.shape, index)
             self.batch = block_table.shape[0]
             self.desc = lyc_layer_cache(
-                k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), 0, st[2], st[1], st[0], 0, ss[2], ss[1], ss[0],
-                block_table.data_ptr(), 0, pages, page_rows, block_table.shape[1], kind, self.batch, self.heads, self.d,
-                self.device_index)
+                kp, vp, ksp, vsp, 0, st[2], st[1], st[0], 0, ss[2], ss[1], ss[0],
+                bt, 0, pages, page_rows, block_table.shape[1], kind, self.batch, self.heads, self.d, index)
+        self._desc_ref = ctypes.byref(self.desc)
+        self._workspace = {}  # bytes by (T, query heads)
 
     @staticmethod
     def empty(batch, heads, d, rows=None, page_rows=None, num_pages=None, block_table=None, e4m3=True, device="cuda"):
@@ -651,39 +655,47 @@ def qk_norm_rope(q, k, pos, inv_freq, q_out, k_out, q_weight=None, k_weight=None
     x = q if q is not None else k
     if x is None or x.dim() != 3:
         _refuse(where, "q or k must be a [rows][heads][d] tensor")
-    index, rows, d, dtype = x.device.index, x.shape[0], x.shape[2], x.dtype
-    if dtype not in (torch.bfloat16, torch.float32):
-        _refuse(where, f"{dtype} is neither bfloat16 nor float32")
-    _same_device(where, index, q=q, k=k, pos=pos, inv_freq=inv_freq, q_out=q_out, k_out=k_out, q_weight=q_weight,
-                 k_weight=k_weight)
-    st = []
-    for name, a, b, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
-        if a is None:
-            if b is not None or w is not None:
-                _refuse(where, f"{name}_out or {name}_weight without {name}")
-            st.append((0, 0, 0, 0, 0))
-            continue
-        if b is None:
-            _refuse(where, f"{name} without {name}_out")
-        shape = (rows, a.shape[1], d) if a.dim() == 3 else (rows, 0, d)
-        _rows_in(where, name, a, dtype, shape)
-        _rows_in(where, name + "_out", b, dtype, shape)
-        if w is not None:
-            _packed(where, name + "_weight", w, dtype, (d,))
-        sa, sb = a.stride(), b.stride()
-        st.append((sa[0], sa[1], sb[0], sb[1], shape[1]))
-    rot = 0
+    rows, _, d = x.shape
+    dtype, index = x.dtype, x.get_device()
+    if index < 0 or (dtype is not torch.bfloat16 and dtype is not torch.float32):
+        _refuse(where, f"{dtype} on {x.device}: bfloat16 or float32 on a GPU is needed")
+    weight = (d,)
+    qp = qo = kp = ko = qw = kw = hq = hk = 0
+    sq = sqo = sk = sko = (0, 0, 0)
+    if q is not None:
+        if q_out is None:
+            _refuse(where, "q without q_out")
+        hq = q.shape[1]
+        shape = (rows, hq, d)
+        qp, sq = _rows_in(where, "q", q, dtype, shape, index)
+        qo, sqo = _rows_in(where, "q_out", q_out, dtype, shape, index)
+        qw = _packed(where, "q_weight", q_weight, dtype, weight, index)
+    elif q_out is not None or q_weight is not None:
+        _refuse(where, "q_out or q_weight without q")
+    if k is not None:
+        if k_out is None or k.dim() != 3:
+            _refuse(where, "k must be a [rows][heads][d] tensor and have a k_out")
+        hk = k.shape[1]
+        shape = (rows, hk, d)
+        kp, sk = _rows_in(where, "k", k, dtype, shape, index)
+        ko, sko = _rows_in(where, "k_out", k_out, dtype, shape, index)
+        kw = _packed(where, "k_weight", k_weight, dtype, weight, index)
+    elif k_out is not None or k_weight is not None:
+        _refuse(where, "k_out or k_weight without k")
+    rot = fp = pp = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _packed(where, "inv_freq", inv_freq, torch.float32, (rot // 2,))
+        half = inv_freq.numel()
+        rot = 2 * half
         if pos is None:
             _refuse(where, "a rotation needs pos")
-        _packed(where, "pos", pos, torch.int32, (rows,))
-    args = lyc_rope_args(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), st[0][0], st[0][1], st[1][0], st[1][1],
-                         st[0][2], st[0][3], st[1][2], st[1][3], _ptr(pos) if rot else None, _ptr(inv_freq),
-                         _ptr(q_weight), _ptr(k_weight), rows, st[0][4], st[1][4], d, rot, int(interleaved), eps,
-                         LYC_BF16 if dtype == torch.bfloat16 else LYC_FP32, index)
-    _operator_check(lyc_qk_norm_rope(args, _stream_on(index, stream)), "lyc_qk_norm_rope")
+        fp = _packed(where, "inv_freq", inv_freq, torch.float32, (half,), index)
+        pp = _packed(where, "pos", pos, torch.int32, (rows,), index)
+    args = _ROPE_ARGS.pack(qp, kp, qo, ko, sq[0], sq[1], sk[0], sk[1], sqo[0], sqo[1], sko[0], sko[1], pp, fp, qw, kw,
+                           rows, hq, hk, d, rot, 1 if interleaved else 0, eps,
+                           LYC_BF16 if dtype is torch.bfloat16 else LYC_FP32, index)
+    rc = _operators().lyc_qk_norm_rope(args, _stream_on(index, stream))
+    if rc:
+        _operator_check(rc, "lyc_qk_norm_rope")
 
 
 def cache_append(cache, n, k, v, t_len=None, q=None, q_out=None, pos=None, inv_freq=None, q_weight=None,
@@ -695,41 +707,38 @@ def cache_append(cache, n, k, v, t_len=None, q=None, q_out=None, pos=None, inv_f
     n, t_len: int32 [B] on the device; pos: int32 [B][T], default the row."""
     import torch
     where = "cache_append"
-    index = cache.device_index
+    index, bf16, i32, B, d = cache.device_index, torch.bfloat16, torch.int32, cache.batch, cache.d
     if k.dim() != 4:
         _refuse(where, "k must be [B][T][Hkv][d]")
-    T, bf16 = k.shape[1], torch.bfloat16
-    shape = (cache.batch, T, cache.heads, cache.d)
-    _same_device(where, index, n=n, k=k, v=v, t_len=t_len, q=q, q_out=q_out, pos=pos, inv_freq=inv_freq,
-                 q_weight=q_weight, k_weight=k_weight)
-    _rows_in(where, "k", k, bf16, shape)
-    _rows_in(where, "v", v, bf16, shape)
-    _packed(where, "n", n, torch.int32, (cache.batch,))
-    if t_len is not None:
-        _packed(where, "t_len", t_len, torch.int32, (cache.batch,))
-    hq, sq, sqo = 0, (0, 0, 0), (0, 0, 0)
+    T = k.shape[1]
+    shape = (B, T, cache.heads, d)
+    kp, sk = _rows_in(where, "k", k, bf16, shape, index)
+    vp, sv = _rows_in(where, "v", v, bf16, shape, index)
+    hq = qp = qo = qw = 0
+    sq = sqo = (0, 0, 0)
     if q is not None:
         if q_out is None or q.dim() != 4:
             _refuse(where, "q must be [B][T][Hq][d] and have a q_out")
         hq = q.shape[2]
-        _rows_in(where, "q", q, bf16, (cache.batch, T, hq, cache.d))
-        _rows_in(where, "q_out", q_out, bf16, q.shape)
-        sq, sqo = q.stride(), q_out.stride()
-    rot = 0
+        shape = (B, T, hq, d)
+        qp, sq = _rows_in(where, "q", q, bf16, shape, index)
+        qo, sqo = _rows_in(where, "q_out", q_out, bf16, shape, index)
+        qw = _packed(where, "q_weight", q_weight, bf16, (d,), index)
+    elif q_out is not None or q_weight is not None:
+        _refuse(where, "q_out or q_weight without q")
+    rot = fp = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _packed(where, "inv_freq", inv_freq, torch.float32, (rot // 2,))
-    if pos is not None:
-        _packed(where, "pos", pos, torch.int32, (cache.batch, T))
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _packed(where, name, w, bf16, (cache.d,))
-    sk, sv = k.stride(), v.stride()
-    args = lyc_append_args(k.data_ptr(), v.data_ptr(), _ptr(q), _ptr(q_out), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2],
-                           sq[0], sq[1], sq[2], sqo[0], sqo[1], sqo[2], n.data_ptr(), _ptr(t_len), _ptr(pos),
-                           _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), T, hq, rot, int(interleaved), eps,
-                           _status_ptr(where, status, index))
-    _operator_check(lyc_cache_append(cache.desc, args, _stream_on(index, stream)), "lyc_cache_append")
+        half = inv_freq.numel()
+        rot = 2 * half
+        fp = _packed(where, "inv_freq", inv_freq, torch.float32, (half,), index)
+    args = _APPEND_ARGS.pack(
+        kp, vp, qp, qo, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], sq[0], sq[1], sq[2], sqo[0], sqo[1], sqo[2],
+        _packed(where, "n", n, i32, (B,), index), _packed(where, "t_len", t_len, i32, (B,), index),
+        _packed(where, "pos", pos, i32, (B, T), index), fp, qw, _packed(where, "k_weight", k_weight, bf16, (d,), index),
+        T, hq, rot, 1 if interleaved else 0, eps, _status_ptr(where, status, index))
+    rc = _operators().lyc_cache_append(cache._desc_ref, args, _stream_on(index, stream))
+    if rc:
+        _operator_check(rc, "lyc_cache_append")
 
 
 def cache_read(cache, n, k_out, v_out, sets=None, first=0, status=None, stream=None):
@@ -738,23 +747,21 @@ def cache_read(cache, n, k_out, v_out, sets=None, first=0, status=None, stream=N
     sets int32 [B][H][m] (H a multiple of Hkv: the step's S) (lyc_cache_read)."""
     import torch
     where = "cache_read"
-    index = cache.device_index
-    if k_out.dim() != 4 or k_out.dtype not in (torch.bfloat16, torch.float32):
+    index, B, dtype = cache.device_index, cache.batch, k_out.dtype
+    if k_out.dim() != 4 or (dtype is not torch.bfloat16 and dtype is not torch.float32):
         _refuse(where, "k_out must be a [B][H][m][d] bf16 or fp32 tensor")
-    H, m = k_out.shape[1], k_out.shape[2]
-    _same_device(where, index, n=n, k_out=k_out, v_out=v_out, sets=sets)
-    _rows_in(where, "k_out", k_out, k_out.dtype, (cache.batch, H, m, cache.d))
-    _rows_in(where, "v_out", v_out, k_out.dtype, k_out.shape)
-    if k_out.stride() != v_out.stride():
+    _, H, m, _ = k_out.shape
+    shape = (B, H, m, cache.d)
+    kp, so = _rows_in(where, "k_out", k_out, dtype, shape, index)
+    vp, sv = _rows_in(where, "v_out", v_out, dtype, shape, index)
+    if so != sv:
         _refuse(where, "k_out and v_out must have the same strides")
-    _packed(where, "n", n, torch.int32, (cache.batch,))
-    if sets is not None:
-        _packed(where, "sets", sets, torch.int32, (cache.batch, H, m))
-    so = k_out.stride()
-    args = lyc_read_args(k_out.data_ptr(), v_out.data_ptr(), so[0], so[1], so[2], n.data_ptr(), _ptr(sets), int(first),
-                         m, H, LYC_BF16 if k_out.dtype == torch.bfloat16 else LYC_FP32,
-                         _status_ptr(where, status, index))
-    _operator_check(lyc_cache_read(cache.desc, args, _stream_on(index, stream)), "lyc_cache_read")
+    args = _READ_ARGS.pack(kp, vp, so[0], so[1], so[2], _packed(where, "n", n, torch.int32, (B,), index),
+                           _packed(where, "sets", sets, torch.int32, (B, H, m), index), first, m, H,
+                           LYC_BF16 if dtype is torch.bfloat16 else LYC_FP32, _status_ptr(where, status, index))
+    rc = _operators().lyc_cache_read(cache._desc_ref, args, _stream_on(index, stream))
+    if rc:
+        _operator_check(rc, "lyc_cache_read")
 
 
 def tree_attention(q, cache, n, out, mask=None, t_len=None, scale=None, workspace=None, status=None, stream=None):
@@ -767,40 +774,41 @@ def tree_attention(q, cache, n, out, mask=None, t_len=None, scale=None, workspac
     allocator for this call."""
     import torch
     where = "tree_attention"
-    index = cache.device_index
+    index, bf16, i32, B = cache.device_index, torch.bfloat16, torch.int32, cache.batch
     if q.dim() != 4:
         _refuse(where, "q must be [B][T][Hq][d]")
-    T, hq = q.shape[1], q.shape[2]
-    _same_device(where, index, q=q, n=n, out=out, mask=mask, t_len=t_len, workspace=workspace)
-    _rows_in(where, "q", q, torch.bfloat16, (cache.batch, T, hq, cache.d))
-    _rows_in(where, "out", out, torch.bfloat16, q.shape)
-    _packed(where, "n", n, torch.int32, (cache.batch,))
-    if t_len is not None:
-        _packed(where, "t_len", t_len, torch.int32, (cache.batch,))
+    _, T, hq, _ = q.shape
+    shape = (B, T, hq, cache.d)
+    qp, sq = _rows_in(where, "q", q, bf16, shape, index)
+    op, so = _rows_in(where, "out", out, bf16, shape, index)
+    mp = 0
     if mask is not None:
-        if mask.dtype not in (torch.int64, torch.uint64):
-            _refuse(where, f"mask is {mask.dtype}, not int64")
-        _packed(where, "mask", mask, mask.dtype, (cache.batch, T, -(-T // 64)))
+        mp = _packed(where, "mask", mask, torch.uint64 if mask.dtype is torch.uint64 else torch.int64,
+                     (B, T, (T + 63) // 64), index)
     if workspace is None:
         need = tree_workspace_bytes(cache, T, hq)
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty((need + 1) // 2)
         else:
             with torch.cuda.stream(stream):  # the allocator orders its reuse on the call's stream
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        _refuse(where, "workspace must be contiguous")
-    sq, so = q.stride(), out.stride()
-    args = lyc_tree_args(q.data_ptr(), out.data_ptr(), sq[0], sq[1], sq[2], so[0], so[1], so[2], n.data_ptr(),
-                         _ptr(t_len), _ptr(mask), T, hq, cache.d**-0.5 if scale is None else scale,
-                         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                         _status_ptr(where, status, index))
-    _operator_check(lyc_tree_attention(cache.desc, args, _stream_on(index, stream)), "lyc_tree_attention")
+                workspace = q.new_empty((need + 1) // 2)
+    elif not workspace.is_contiguous() or workspace.get_device() != index:
+        _refuse(where, f"workspace must be contiguous, on cuda:{index}")
+    args = _TREE_ARGS.pack(qp, op, sq[0], sq[1], sq[2], so[0], so[1], so[2], _packed(where, "n", n, i32, (B,), index),
+                           _packed(where, "t_len", t_len, i32, (B,), index), mp, T, hq,
+                           cache.d**-0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes,
+                           _status_ptr(where, status, index))
+    rc = _operators().lyc_tree_attention(cache._desc_ref, args, _stream_on(index, stream))
+    if rc:
+        _operator_check(rc, "lyc_tree_attention")
 
 
 def tree_workspace_bytes(cache, T: int, num_q_heads: int) -> int:
     """Bytes of tree_attention's workspace for q [B][T][num_q_heads][d] over `cache`."""
-    need = lyc_tree_workspace_bytes(cache.desc, T, num_q_heads)
-    if need == 0:
-        raise LycError(LYC_ERR_INVALID_ARG, "lyc_tree_workspace_bytes", lyc_operator_error())
+    need = cache._workspace.get((T, num_q_heads))
+    if need is None:
+        need = lyc_tree_workspace_bytes(cache.desc, T, num_q_heads)
+        if need == 0:
+            raise LycError(LYC_ERR_INVALID_ARG, "lyc_tree_workspace_bytes", lyc_operator_error())
+        cache._workspace[(T, num_q_heads)] = need
     return need

@@ -137,11 +137,11 @@ def test_bad_tree(lyc, kw, code):
 def test_null_structs_and_nothing_to_do(lyc):
     lib = lyc.load()
     assert lib.lyc_qk_norm_rope(None, None) == -1
-    assert lib.lyc_cache_append(None, append(lyc), None) == -1
+    assert lib.lyc_cache_append(None, ctypes.byref(append(lyc)), None) == -1
     assert lib.lyc_cache_append(cache(lyc), None, None) == -1
     assert lib.lyc_cache_read(cache(lyc), None, None) == -1
     assert lib.lyc_tree_attention(cache(lyc), None, None) == -1
-    assert lib.lyc_tree_attention(None, tree(lyc), None) == -1
+    assert lib.lyc_tree_attention(None, ctypes.byref(tree(lyc)), None) == -1
     # no rows: nothing is enqueued, and no device is needed
     assert lyc.lyc_qk_norm_rope(rope(lyc, rows=0), None) == 0
     assert lyc.lyc_cache_read(cache(lyc), read(lyc, m=0), None) == 0
