@@ -116,6 +116,15 @@ CacheView view(const lyc_layer_cache* c) {
   w.num_pages = c->num_pages;
   w.page_rows = c->page_rows;
   w.max_blocks = c->max_blocks;
+  // with s = ceil(log2 d) and m = ceil(2^(30+s) / d), m d = 2^(30+s) + r, r < d <= 2^s:
+  // n m / 2^(30+s) exceeds n / d by n r / (d 2^(30+s)) < 1 / d, so its floor is right
+  w.page_mul = w.page_shift = 0;
+  if (c->block_table) {
+    uint32_t s = 0;
+    while ((1u << s) < static_cast<uint32_t>(c->page_rows)) ++s;
+    w.page_shift = 30 + s;
+    w.page_mul = static_cast<uint32_t>(((1ull << w.page_shift) + c->page_rows - 1) / c->page_rows);
+  }
   w.cap = static_cast<int32_t>(c->block_table ? static_cast<int64_t>(c->page_rows) * c->max_blocks : c->rows);
   return w;
 }
@@ -159,7 +168,8 @@ bool tree_shape(const lyc_layer_cache* c, int T, int Hq, bool may_tc, TreeShape*
   const int sms = sm_count(c->device);
   if (sms < 1) return false;
   const int rows = Hq / c->num_kv_heads * T;
-  s->tc = may_tc && c->head_dim == 128 && rows > kMmaMostRows && tree_tc_box_rows(view(c)) > 0;
+  s->tc = may_tc && c->head_dim == 128 && rows > kMmaMostRows &&
+          (c->type == LYC_CACHE_E4M3 || tree_tc_box_rows(view(c)) > 0);
   s->block_rows = s->tc ? 128 : tree_mma_block_rows(rows);
   s->tile_rows = s->tc ? 128 : tree_mma_tile_rows(c->head_dim, c->type);
   s->mblocks = (rows + s->block_rows - 1) / s->block_rows;
@@ -413,10 +423,10 @@ lyc_status lyc_tree_attention(const lyc_layer_cache* c, const lyc_tree_args* a, 
   p.G = a->num_q_heads / c->num_kv_heads;
   p.scale_log2 = a->scale * 1.4426950408889634f;
   p.cache = view(c);
-  if (s.tc) {
+  if (s.tc && c->type == LYC_CACHE_BF16) {
     p.box_rows = tree_tc_box_rows(p.cache);
     // a layout that TMA cannot describe (a stride of 2^40 bytes, say); needs no more workspace
-    if (!tree_tc_maps(&P, c->type)) tree_shape(c, a->T, a->num_q_heads, false, &s);
+    if (!tree_tc_maps(&P)) tree_shape(c, a->T, a->num_q_heads, false, &s);
   }
   p.grid = s.grid;
   p.part_o = static_cast<float*>(a->workspace);

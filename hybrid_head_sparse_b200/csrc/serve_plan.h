@@ -23,7 +23,13 @@ struct CacheView {
   int64_t num_pages;
   int32_t page_rows, max_blocks;
   int32_t cap;  // rows an element can hold
+  // row / page_rows = row * page_mul >> page_shift, for rows below 2^30
+  uint32_t page_mul, page_shift;
 };
+
+__device__ __forceinline__ int page_of(const CacheView& c, int row) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(row)) * c.page_mul) >> c.page_shift);
+}
 
 // Offsets of row i of element b's head 0 in K/V (elements) and in the scales;
 // false where the block table names no page of the pool.
@@ -36,7 +42,7 @@ __device__ __forceinline__ bool cache_row(const CacheView& c, int b, int i, RowA
     at->sc = b * c.ss_batch + i * c.ss_token;
     return true;
   }
-  const int blk = i / c.page_rows, r = i - blk * c.page_rows;
+  const int blk = page_of(c, i), r = i - blk * c.page_rows;
   const int32_t page = c.bt[static_cast<int64_t>(b) * c.max_blocks + blk];
   if (page < 0 || page >= c.num_pages) return false;
   at->kv = page * c.s_page + r * c.s_token;
@@ -95,7 +101,7 @@ struct TreeParams {
   float2* part_ml;  // [2 * grid][rows per block]: running maximum (log2 units) and sum
   int32_t B, T, W, Hq, Hkv, G;
   int32_t grid;
-  int32_t box_rows;  // tcgen05 kernel: rows of one TMA box
+  int32_t box_rows;  // tcgen05 kernel, bf16: rows of one TMA box
   float scale_log2;
   CacheView cache;
 };
@@ -116,7 +122,7 @@ cudaError_t tree_mma_launch(const TreeParams* p, int head_dim, int cache_type, i
                             cudaStream_t stream);
 // tree_tc_kernel.cu: head_dim 128; 128 rows a tile, 128 query rows a block
 int tree_tc_box_rows(const CacheView& c);
-bool tree_tc_maps(TreeTcParams* P, int cache_type);
+bool tree_tc_maps(TreeTcParams* P);
 cudaError_t tree_tc_launch(const TreeTcParams* P, int cache_type, int device, cudaStream_t stream);
 cudaError_t tree_combine_launch(const TreeParams* p, int head_dim, int block_rows, int tile_rows,
                                 cudaStream_t stream);

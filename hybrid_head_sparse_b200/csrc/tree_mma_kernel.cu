@@ -240,12 +240,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
       tree_elem(p, b, &bad);
       if (bad) atomicOr(p.status, LYC_OP_BAD_LENGTH);
     }
-  TreeWalk<C::TR, C::ROWS> walk(p);
+  const TreeSched<C::TR, C::ROWS> sched(p);
   const int cta = blockIdx.x;
   const float NEG = -INFINITY;
-  TreePiece pc;
+  const uint32_t xend = sched.begin(cta + 1);
 
-  while (walk.next(&pc)) {
+  for (uint32_t x = sched.begin(cta); x < xend;) {
+    const TreePiece pc = piece_at(sched, x, xend);
+    x += pc.t1 - pc.t0;
     const int first_draft = pc.e.n - pc.e.cnt;
     TmLoader<C> ld(p, pc, smem, warp, lane);
     ld.look_up(0);

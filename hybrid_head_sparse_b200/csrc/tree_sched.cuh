@@ -157,29 +157,52 @@ struct TreePiece {
   TreeElem e;
 };
 
+// The piece that holds tile x of a run that ends at xend.
+template <int TR, int ROWS>
+__device__ __forceinline__ TreePiece piece_at(const TreeSched<TR, ROWS>& sched, uint32_t x, uint32_t xend) {
+  TreePiece pc;
+  uint32_t first;
+  sched.locate(x, &pc.b, &first);
+  pc.e = sched.elem(pc.b);
+  pc.nt = (pc.e.n + TR - 1) / TR;
+  const uint32_t rel = x - first, nt = static_cast<uint32_t>(pc.nt);
+  const int grp = static_cast<int>(rel / nt);
+  const int mbs = sched.blocks(pc.e);
+  pc.g = mbs == 1 ? grp : grp / mbs;
+  pc.mb = grp - pc.g * mbs;
+  pc.t0 = static_cast<int>(rel - static_cast<uint32_t>(grp) * nt);
+  pc.t1 = static_cast<int>(min(nt, pc.t0 + (xend - x)));
+  return pc;
+}
+
+// As calls, not inlined: each role of the tcgen05 kernel walks the run, and with
+// the walk in each of them its loops lie far apart in the instruction caches.
+template <int TR, int ROWS>
+__device__ __noinline__ TreePiece tree_piece(const TreeParams& p, uint32_t x) {
+  const TreeSched<TR, ROWS> sched(p);
+  return piece_at(sched, x, sched.begin(blockIdx.x + 1));
+}
+template <int TR, int ROWS>
+__device__ __noinline__ uint2 tree_run(const TreeParams& p) {
+  const TreeSched<TR, ROWS> sched(p);
+  return make_uint2(sched.begin(blockIdx.x), sched.begin(blockIdx.x + 1));
+}
+
 // The pieces of this CTA's run in order.
 template <int TR, int ROWS>
 struct TreeWalk {
   const TreeParams& p;
-  TreeSched<TR, ROWS> sched;
   uint32_t x, xend;
-  __device__ __forceinline__ explicit TreeWalk(const TreeParams& prm) : p(prm), sched(prm) {
-    x = sched.begin(blockIdx.x);
-    xend = sched.begin(blockIdx.x + 1);
+  __device__ __forceinline__ explicit TreeWalk(const TreeParams& prm) : p(prm) {
+    const uint2 run = tree_run<TR, ROWS>(prm);
+    x = run.x;
+    xend = run.y;
   }
+  // tiles of the run; before the first next()
+  __device__ __forceinline__ uint32_t run_tiles() const { return xend - x; }
   __device__ __forceinline__ bool next(TreePiece* pc) {
     if (x >= xend) return false;
-    uint32_t first;
-    sched.locate(x, &pc->b, &first);
-    pc->e = sched.elem(pc->b);
-    pc->nt = (pc->e.n + TR - 1) / TR;
-    const uint32_t rel = x - first, nt = static_cast<uint32_t>(pc->nt);
-    const int grp = static_cast<int>(rel / nt);
-    const int mbs = sched.blocks(pc->e);
-    pc->g = mbs == 1 ? grp : grp / mbs;
-    pc->mb = grp - pc->g * mbs;
-    pc->t0 = static_cast<int>(rel - static_cast<uint32_t>(grp) * nt);
-    pc->t1 = static_cast<int>(min(nt, pc->t0 + (xend - x)));
+    *pc = tree_piece<TR, ROWS>(p, x);
     x += pc->t1 - pc->t0;
     return true;
   }

@@ -22,12 +22,13 @@
 // the end, and take a drafted row's NaNs and infinities out of V; the nodes
 // that see such a row get them added at the end.
 //
-// e4m3 rows: K's codes are the B operand as they are (kind::f8f6f4), against
-// the query row in two e4m3 terms, high and low (four significant bits each,
-// a bf16 query's eight; what is below 2^-17 of the row's largest element is
-// rounded there).  V's codes become f16 on their way through four converter
-// warps (value * 2^-8, exact), P is f16.  V's scales go into the exponent and
-// K's into the logit, as in tree_mma_kernel.cu.
+// e4m3 rows become bf16 on their way into the same tiles (code * 2^e, exact),
+// so nothing after the tiles knows the difference.  Eight producer warps find the
+// rows of coming tiles, ask L2 for them and read their scales, load 16 codes a
+// lane and instruction, convert and store them.  (Scales
+// applied to logits and probabilities instead, K's codes as an e4m3 operand,
+// took 5000 cycles a tile against about 2000: shared memory was what it waited
+// for, with the tensor core's reads, the conversion's and the scales' on it.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -47,37 +48,36 @@ namespace {
 constexpr int kRows = 128;  // query rows of a block, cached rows of a tile
 constexpr int kD = 128;
 constexpr int kSoft = 256;  // softmax threads
-constexpr int kOkRing = 8;
+constexpr int kOkRing = 16;
+constexpr int kRawRing = 2;    // e4m3: tiles of codes on their way
+constexpr int kProducers = 8;  // warps
+constexpr int kUnits = 32 / kProducers;  // 4-row units of a K tile, and of a V tile, of each
 
 template <bool F8_>
 struct TcCfg {
   static constexpr bool F8 = F8_;
-  static constexpr int SK = F8 ? 4 : 3;              // K tiles in flight
-  static constexpr int SV = F8 ? 3 : 3;              // V tiles in flight
-  static constexpr int SC = 2;                       // converted V tiles (F8)
-  static constexpr int NS = 4;                       // tiles of scales (F8)
-  static constexpr int TILEB = F8 ? 16384 : 32768;   // a K or V tile as it lies in the cache
-  static constexpr int CONV = F8 ? 128 : 0;          // converter threads
-  static constexpr int THREADS = kSoft + 64 + CONV;
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, CONV_WARP = 10;
-  static constexpr int OFF_Q = 0;                    // bf16 32 KiB; F8: high terms, low terms
+  static constexpr int SK = F8 ? 2 : 3;              // K tiles
+  static constexpr int SV = F8 ? 2 : 3;              // V tiles
+  static constexpr int TILEB = 32768;                // a K or V tile of bf16
+  static constexpr int THREADS = 9 * 32 + (F8 ? kProducers * 32 : 32);
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9;  // F8: LOAD_WARP is the first producer
+  static constexpr int FULL = F8 ? kProducers : 1;      // arrivals that fill a tile
+  static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 32768;
   static constexpr int OFF_V = OFF_K + SK * TILEB;
-  static constexpr int OFF_VC = OFF_V + SV * TILEB;
-  static constexpr int OFF_SCALE = OFF_VC + (F8 ? SC * 32768 : 0);  // [NS][3][128] floats
-  static constexpr int OFF_BAR = OFF_SCALE + (F8 ? NS * 3 * 512 : 0);
+  static constexpr int OFF_RAW = OFF_V + SV * TILEB;  // F8: codes, [producer][kRawRing][K, V][unit][lane] of 16 bytes
+  static constexpr int OFF_BAR = OFF_RAW + (F8 ? kRawRing * 32768 : 0);
   // kfull, kempty [SK]; vfull, vempty [SV]; s_ready, p_ready, pv_done [2];
-  // q_ready, o_free, ml_ready, idle; F8: vc_full, vc_empty [SC], sc_full [NS]
-  static constexpr int NBAR = 2 * SK + 2 * SV + 6 + 4 + (F8 ? 2 * SC + NS : 0);
-  static constexpr int OFF_FLAGS = OFF_BAR + NBAR * 8;  // abort, tmem, odd rows [2][8], ok [kOkRing]
-  static constexpr int SMEM = OFF_FLAGS + 8 + 64 + 4 * kOkRing + 1024;  // + alignment
+  // q_ready, o_free, ml_ready, idle
+  static constexpr int NBAR = 2 * SK + 2 * SV + 6 + 4;
+  static constexpr int OFF_FLAGS = OFF_BAR + NBAR * 8;  // abort, tmem, odd rows [2][8], ok [kOkRing][8]
+  static constexpr int SMEM = OFF_FLAGS + 8 + 64 + 32 * kOkRing + 1024;  // + alignment
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
 template <class C>
 struct TcBars {
-  uint64_t *kfull, *kempty, *vfull, *vempty, *s_ready, *p_ready, *pv_done, *q_ready, *o_free, *ml_ready, *idle,
-      *vc_full, *vc_empty, *sc_full;
+  uint64_t *kfull, *kempty, *vfull, *vempty, *s_ready, *p_ready, *pv_done, *q_ready, *o_free, *ml_ready, *idle;
   __device__ explicit TcBars(unsigned char* smem) {
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     kfull = b;
@@ -91,9 +91,6 @@ struct TcBars {
     o_free = q_ready + 1;
     ml_ready = o_free + 1;
     idle = ml_ready + 1;
-    vc_full = idle + 1;
-    vc_empty = vc_full + (C::F8 ? C::SC : 0);
-    sc_full = vc_empty + (C::F8 ? C::SC : 0);
   }
 };
 
@@ -101,7 +98,7 @@ struct TcShared {
   int* abort;
   uint32_t* tmem;
   uint32_t* odd;  // [2] by piece: drafted rows with a NaN or an infinity in V, by node
-  uint32_t* ok;   // ring of the tiles' boxes that were found
+  uint32_t* ok;   // ring of the tiles' rows that were found (paged), 8 words each
 };
 template <class C>
 __device__ __forceinline__ TcShared shared_of(unsigned char* smem) {
@@ -115,12 +112,18 @@ __device__ __forceinline__ TcShared shared_of(unsigned char* smem) {
 
 // Wait for a phase of `bar`; false once the CTA has given up (a wait above
 // kWaitLimitNs).  heed: also give up where another warp has.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* status,
-                                        bool heed = true) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool tc_wait_on(uint32_t bar, uint32_t parity, int* abort_flag, uint32_t* status, bool heed) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
     if ((i & 1023u) == 0) {
       if (heed && *reinterpret_cast<volatile int*>(abort_flag)) return false;
       const uint64_t now = global_timer_ns();
@@ -133,6 +136,18 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* abo
       }
     }
   }
+}
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, int* abort_flag, uint32_t* status,
+                                        bool heed = true) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return tc_wait_on(smem_u32(bar), parity, abort_flag, status, heed);
+}
+
+// One arrival for a warp, after all its lanes' earlier accesses.  (Arrivals of 32
+// lanes on one barrier are taken one after another.)
+__device__ __forceinline__ void tc_arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // The same for a whole warp, which goes on or gives up together.
@@ -160,13 +175,9 @@ __device__ __forceinline__ float tc_ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-template <bool F16>
 __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
   uint32_t r;
-  if (F16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 __device__ __forceinline__ void tc_st_x16(uint32_t taddr, const uint32_t* r) {
@@ -190,7 +201,28 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (*r)[16]) {
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands
+// Two fp32 operations an instruction (sm_100's packed forms).
+typedef unsigned long long f2_t;
+__device__ __forceinline__ f2_t f2(float a, float b) {
+  f2_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_split(f2_t r, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(r));
+}
+__device__ __forceinline__ f2_t f2_fma(f2_t a, f2_t b, f2_t c) {
+  f2_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2_t f2_add(f2_t a, f2_t b) {
+  f2_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 operands
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -199,24 +231,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, K = 32
-__device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// fp32 sums, M = N = 128; bits 7-9 and 10-12 the types of A and B (f16 0, bf16 1; e4m3 0)
-__host__ __device__ constexpr uint32_t idesc128(uint32_t type, int b_mn_major) {
-  return (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(b_mn_major) << 16) | ((128u >> 3) << 17) |
-         ((128u >> 4) << 24);
-}
 
 typedef TreeWalk<kRows, kRows> TcWalk;
 
-// ---------------------------------------------------------------- loads
+// ---------------------------------------------------------------- loads (bf16)
 // The whole warp: lane j looks up and copies box j of a tile (one box of 128
 // rows where the cache is contiguous, else box_rows rows of a page).
 template <class C>
@@ -228,7 +246,7 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
   // a cache that several blocks of query rows read stays in L2
   const uint64_t pol = p.G * p.T > kRows ? l2_policy_evict_normal() : l2_policy_evict_first();
   const bool paged = p.cache.bt != nullptr;
-  const int nbox = kRows / P.t.box_rows;
+  const int nbox = kRows / p.box_rows;
   const uint32_t boxb = static_cast<uint32_t>(C::TILEB) / nbox;  // bytes of a box
   TcWalk walk(p);
   TreePiece pc;
@@ -237,11 +255,11 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
   bool ok = true;
   while (ok && walk.next(&pc)) {
     for (int tile = pc.t0; ok && tile < pc.t1; ++tile, ++t) {
-      const int row0 = tile * kRows + lane * P.t.box_rows;
+      const int row0 = tile * kRows + lane * p.box_rows;
       bool have = lane < nbox && row0 < pc.e.n;
       int c1 = row0, c2 = pc.g, c3 = pc.b;
       if (paged && have) {
-        const int blk = row0 / p.cache.page_rows;
+        const int blk = page_of(p.cache, row0);
         const int32_t page = p.cache.bt[static_cast<int64_t>(pc.b) * p.cache.max_blocks + blk];
         have = page >= 0 && page < p.cache.num_pages;
         if (!have && p.status) atomicOr(p.status, LYC_OP_BAD_PAGE);
@@ -261,16 +279,20 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
           ok = false;
           break;
         }
-        if (lane == 0) {
-          if (kv == 0) sh.ok[t % kOkRing] = found;
-          mbar_arrive_expect_tx(full, bytes);
+        if (kv == 0 && paged && lane < 4) {
+          uint32_t rows = 0;  // rows 32 lane .. + 31 by their boxes (of 8 rows or more)
+          for (int x = 0; x < 32; x += 8)
+            if ((found >> ((lane * 32 + x) / p.box_rows)) & 1u) rows |= 0xffu << x;
+          sh.ok[(t % kOkRing) * 8 + lane] = rows;
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        __syncwarp();
         if (have) {
-          unsigned char* dst = smem + (kv ? C::OFF_V : C::OFF_K) + stage * C::TILEB + lane * P.t.box_rows * 128;
+          unsigned char* dst = smem + (kv ? C::OFF_V : C::OFF_K) + stage * C::TILEB + lane * p.box_rows * 128;
           const CUtensorMap* map = kv ? &P.tmv : &P.tmk;
           tma_4d(dst, map, 0, c1, c2, c3, full, pol);
-          if (!C::F8) tma_4d(dst + 16384, map, 64, c1, c2, c3, full, pol);
+          tma_4d(dst + 16384, map, 64, c1, c2, c3, full, pol);
         }
         asked[kv] = t + 1;
         __syncwarp();
@@ -289,19 +311,230 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
   }
 }
 
+// ---------------------------------------------------------------- producers (e4m3)
+// Four e4m3 codes as bf16 of value * 2^-120 (sign; exponent and mantissa bits
+// where bf16 has the low ones of its exponent and the high ones of its
+// mantissa): codes 0 and 2, codes 1 and 3.  The columns of K and of V come out
+// with 4w + {1, 2} exchanged, and Q's and O's with them.
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t* h02, uint32_t* h13) {
+  const uint32_t x = w << 8;
+  *h02 = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
+  *h13 = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 16 codes at scale byte e as bf16 (two factors: any e).
+__device__ __noinline__ void convert_far(uint4 u, uint32_t e, uint4* lo, uint4* hi) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  const int x = static_cast<int>(e) - 127, x1 = x >> 1;
+  const uint32_t f = e == 255u ? 0x7fff7fffu : (static_cast<uint32_t>(187 + x1) << 7) * 0x10001u;
+  const uint32_t g = e == 255u ? 0x3f803f80u : (static_cast<uint32_t>(187 + x - x1) << 7) * 0x10001u;
+  uint32_t h[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    codes_bf16(w[k], &h[2 * k], &h[2 * k + 1]);
+    h[2 * k] = mul_bf16x2(mul_bf16x2(h[2 * k], g), f);
+    h[2 * k + 1] = mul_bf16x2(mul_bf16x2(h[2 * k + 1], g), f);
+  }
+  *lo = make_uint4(h[0], h[1], h[2], h[3]);
+  *hi = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// The rows of one producer warp, one a lane: the page of a tile's row is asked for
+// one tile before the row's place is computed and its scales are read.
+struct RowSteps {
+  const TreeParams& p;
+  TreeWalk<kRows, kRows> walk;
+  TreePiece pc;
+  bool more;
+  int tiles;         // of the run
+  int tile, row_in;  // the next tile to begin, this lane's row in a tile
+  int32_t page;
+  int64_t kv, sc;    // offsets, less the page's part
+  bool in;           // the row is one of the element's
+
+  __device__ __forceinline__ RowSteps(const TreeParams& prm, int r) : p(prm), walk(prm), tile(0), row_in(r) {
+    tiles = static_cast<int>(walk.run_tiles());
+    more = walk.next(&pc);
+    if (more) tile = pc.t0;
+    in = false;
+    page = 0;
+    kv = sc = 0;
+  }
+  __device__ __forceinline__ void begin() {
+    in = false;
+    if (!more) return;
+    const int row = tile * kRows + row_in;
+    in = row < pc.e.n;
+    kv = pc.g * p.cache.s_head;
+    sc = pc.g * p.cache.ss_head;
+    int r = row;
+    if (p.cache.bt) {
+      const int blk = page_of(p.cache, row);
+      r = row - blk * p.cache.page_rows;
+      page = p.cache.bt[in ? static_cast<int64_t>(pc.b) * p.cache.max_blocks + blk : 0];
+    } else {
+      kv += pc.b * p.cache.s_batch;
+      sc += pc.b * p.cache.ss_batch;
+    }
+    kv += r * p.cache.s_token;
+    sc += r * p.cache.ss_token;
+    if (++tile >= pc.t1) {
+      more = walk.next(&pc);
+      tile = pc.t0;
+    }
+  }
+  // The row's offset in K and V, odd where there is no such row (codes are then
+  // zeros), and its scale bytes (as they come, some row's where there is none:
+  // anything done with them here would wait for them); whether it was found.
+  __device__ __forceinline__ bool find(long long* off, uint32_t* kb, uint32_t* vb) {
+    bool have = in;
+    int64_t o = kv, at = sc;
+    if (p.cache.bt && in) {
+      have = page >= 0 && page < p.cache.num_pages;
+      if (!have && p.status) atomicOr(p.status, LYC_OP_BAD_PAGE);
+      o += page * p.cache.s_page;
+      at += page * p.cache.ss_page;
+    }
+    *off = have ? o : 1;
+    at = have ? at : 0;
+    *kb = p.cache.ks[at];
+    *vb = p.cache.vs[at];
+    return have;
+  }
+};
+
+// Each producer warp has four 4-row units of every K tile and of every V tile,
+// eight lanes a row.  A lane copies its 16 codes of a unit to shared memory two
+// tiles ahead and converts what it copied itself, so a warp waits for nobody's
+// copies but its own.  (With the codes kept in registers instead, the loops had
+// to be unrolled over them and, with the softmax's, outgrew the SM's instruction
+// cache: 7600 cycles a tile, 40% of the instruction fetches missing.)
+template <class C>
+__device__ __forceinline__ void tc_produce(const TreeTcParams& P, unsigned char* smem) {
+  const TreeParams& p = P.t;
+  const int w = (threadIdx.x >> 5) - C::LOAD_WARP, lane = threadIdx.x & 31;
+  // eight adjacent lanes store half a row each of an even and an odd row: with
+  // the swizzle, eight different banks
+  const int c = (lane & 3) | (((lane >> 3) & 1) << 2);
+  const int rr = ((lane >> 4) << 1) | ((lane >> 2) & 1);
+  const int r0 = w * 4 + rr;  // the first unit's row; + 32 for each unit
+  TcBars<C> br(smem);
+  const TcShared sh = shared_of<C>(smem);
+  const uint32_t st0 = tile_off(r0, 2 * c), st1 = tile_off(r0, 2 * c + 1);
+  constexpr int HALFB = kUnits * 512;  // a warp's codes of a K or V tile
+  unsigned char* const raw = smem + C::OFF_RAW + w * (kRawRing * 2 * HALFB) + lane * 16;
+  const unsigned char* const kg = p.cache.k + c * 16;
+  const unsigned char* const vg = p.cache.v + c * 16;
+  // lanes l and l + 16 look after row 32 (l / 4) + 4 w + l % 4: unit l / 4
+  RowSteps st(p, ((lane >> 2) & 3) * 32 + w * 4 + (lane & 3));
+  const int ntile = st.tiles;
+  if (ntile == 0) return;
+  long long off;
+  uint32_t s0 = 0, s1 = 0;     // scale bytes (K's, V's << 8) of this tile's row and the next one's
+  uint32_t kb = 127, vb = 127;  // and those of the one after, on their way
+  bool have = false;
+  // the rows that were found, a word for this warp's 32 rows of a tile
+  auto find = [&](int t) {
+    have = st.find(&off, &kb, &vb);
+    const uint32_t m = __ballot_sync(0xffffffffu, have);
+    if (p.cache.bt && lane == 0) sh.ok[(t % kOkRing) * 8 + w] = m;
+    st.begin();
+  };
+  auto copy = [&](int t) {  // with the offsets just found
+    if (t >= 0 && t < ntile) {
+      const uint32_t dst = smem_u32(raw + (t % kRawRing) * 2 * HALFB);
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) {
+        const long long o = __shfl_sync(0xffffffffu, off, 4 * j + rr);
+        const int n = (o & 1) ? 0 : 16;
+        const long long at = o & ~1ll;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 512), "l"(kg + at), "r"(n) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + HALFB + j * 512), "l"(vg + at), "r"(n)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  st.begin();
+#pragma unroll 1
+  for (int t = -3; t < ntile; ++t) {  // tile t is converted, t + 2 copied, t + 3 found
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRawRing - 1) : "memory");
+    const bool far = __any_sync(0xffffffffu, ((s0 & 255u) > 134u) || ((s0 >> 8) > 134u));
+#pragma unroll 1
+    for (int kv = 0; kv < 2 && t >= 0; ++kv) {
+      const int S = kv ? C::SV : C::SK, stage = t % S;
+      if (t >= S && !tc_wait_warp((kv ? br.vempty : br.kempty) + stage, ((t / S) - 1) & 1, sh.abort, p.status)) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        return;
+      }
+      const unsigned char* src = raw + (t % kRawRing) * 2 * HALFB + kv * HALFB;
+      unsigned char* dst = smem + (kv ? C::OFF_V : C::OFF_K) + stage * C::TILEB;
+      const uint32_t mine = (kv ? s0 >> 8 : s0) & 255u;
+      if (__builtin_expect(far, 0)) {
+#pragma unroll 1
+        for (int j = 0; j < kUnits; ++j) {
+          uint4 lo, hi;
+          convert_far(*reinterpret_cast<const uint4*>(src + j * 512), __shfl_sync(0xffffffffu, mine, 4 * j + rr), &lo, &hi);
+          *reinterpret_cast<uint4*>(dst + st0 + j * 4096) = lo;
+          *reinterpret_cast<uint4*>(dst + st1 + j * 4096) = hi;
+        }
+      } else {
+        const uint32_t factor = ((mine + 120u) << 7) * 0x10001u;  // 2^(120 + e - 127) twice
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+          const uint4 u = *reinterpret_cast<const uint4*>(src + j * 512);
+          const uint32_t f = __shfl_sync(0xffffffffu, factor, 4 * j + rr);
+          uint32_t h[8];
+          codes_bf16(u.x, &h[0], &h[1]);
+          codes_bf16(u.y, &h[2], &h[3]);
+          codes_bf16(u.z, &h[4], &h[5]);
+          codes_bf16(u.w, &h[6], &h[7]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f);
+          *reinterpret_cast<uint4*>(dst + st0 + j * 4096) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + st1 + j * 4096) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+      tc::fence_async_smem();
+      tc_arrive_warp((kv ? br.vfull : br.kfull) + stage);
+    }
+    s0 = s1;
+    s1 = have ? kb | (vb << 8) : 127u | (127u << 8);
+    copy(t + 2);
+    find(t + 3);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- MMA warp
 // QK of tile t+1 goes out before the PV of tile t, within a piece (the next
 // piece's queries are written only after this one's last PV), and once the PV
 // of tile t-1, whose P lies in the same columns, is done.
+// (The whole warp waits and keeps the counts, so that the descriptors are uniform
+// values; one elected lane issues.)
+__device__ __forceinline__ bool tc_elect() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 template <class C>
 __device__ __forceinline__ void tc_mma(const TreeTcParams& P, unsigned char* smem, uint32_t tmem) {
   const TreeParams& p = P.t;
-  const int lane = threadIdx.x & 31;
   TcBars<C> br(smem);
   const TcShared sh = shared_of<C>(smem);
-  const uint32_t qbase = smem_u32(smem + C::OFF_Q);
-  const uint32_t kbase = smem_u32(smem + C::OFF_K);
-  const uint32_t vbase = smem_u32(smem + (C::F8 ? C::OFF_VC : C::OFF_V));
+  const uint64_t qd = tc::smem_desc(smem_u32(smem + C::OFF_Q), 16, 1024, 2);
+  const uint64_t kd = tc::smem_desc(smem_u32(smem + C::OFF_K), 16, 1024, 2);
+  const uint64_t vd = tc::smem_desc(smem_u32(smem + C::OFF_V), 16384, 1024, 2);
   TcWalk walk(p);
   TreePiece pc;
   int t = 0, piece = 0;
@@ -309,170 +542,64 @@ __device__ __forceinline__ void tc_mma(const TreeTcParams& P, unsigned char* sme
 
   auto issue_qk = [&](int tt, bool first) -> bool {
     const int stage = tt % C::SK, b = tt & 1;
-    bool go = true;
-    if (lane == 0) {
-      go = (!first || tc_wait(br.q_ready, piece & 1, sh.abort, p.status)) &&
-           (tt < 2 || tc_wait(&br.pv_done[b], ((tt - 2) >> 1) & 1, sh.abort, p.status)) &&
-           tc_wait(&br.kfull[stage], (tt / C::SK) & 1, sh.abort, p.status);
-      if (go) {
-        tc::fence_after_sync();
-        const uint32_t kb = kbase + stage * C::TILEB;
-        if (C::F8) {
+    if (first && !tc_wait_warp(br.q_ready, piece & 1, sh.abort, p.status)) return false;
+    if (tt >= 2 && !tc_wait_warp(&br.pv_done[b], ((tt - 2) >> 1) & 1, sh.abort, p.status)) return false;
+    if (!tc_wait_warp(&br.kfull[stage], (tt / C::SK) & 1, sh.abort, p.status)) return false;
+    tc::fence_after_sync();
+    const uint64_t ks = kd + static_cast<uint32_t>(stage * (C::TILEB >> 4));
+    if (tc_elect()) {
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f8_ss(tmem + b * 128, tc::smem_desc(qbase + term * 16384 + kk * 32, 16, 1024, 2),
-                        tc::smem_desc(kb + kk * 32, 16, 1024, 2), idesc128(0, 0), term + kk > 0 ? 1u : 0u);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            tc::mma_bf16_ss(tmem + b * 128, tc::smem_desc(qbase + off, 16, 1024, 2),
-                            tc::smem_desc(kb + off, 16, 1024, 2), idesc128(1, 0), kk > 0 ? 1u : 0u);
-          }
-        }
-        tc::commit(&br.kempty[stage]);
-        tc::commit(&br.s_ready[b]);
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        tc::mma_bf16_ss(tmem + b * 128, qd + off, ks + off, tc::idesc_bf16(128, 128, 0, 0), kk > 0 ? 1u : 0u);
       }
+      tc::commit(&br.kempty[stage]);
+      tc::commit(&br.s_ready[b]);
     }
-    return __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+    __syncwarp();
+    return true;
   };
 
   while (ok && walk.next(&pc)) {
     const int cnt = pc.t1 - pc.t0;
-    ok = issue_qk(t, true);
-    for (int u = 0; ok && u < cnt; ++u, ++t) {
-      if (u + 1 < cnt) ok = issue_qk(t + 1, false);
+#pragma unroll 1
+    for (int u = -1; ok && u < cnt; ++u) {
+      // the next tile's QK (the first time the piece's first), then this tile's PV
+      if (u + 1 < cnt) ok = issue_qk(t + (u < 0 ? 0 : 1), u < 0);
+      if (!ok || u < 0) continue;
+      const int b = t & 1, vs = t % C::SV;
+      ok = tc_wait_warp(&br.p_ready[b], (t >> 1) & 1, sh.abort, p.status) &&
+           tc_wait_warp(&br.vfull[vs], (t / C::SV) & 1, sh.abort, p.status) &&
+           (u > 0 || piece == 0 || tc_wait_warp(br.o_free, (piece - 1) & 1, sh.abort, p.status));
       if (!ok) break;
-      const int b = t & 1;
-      bool go = true;
-      if (lane == 0) {
-        const int vs = C::F8 ? t % C::SC : t % C::SV;
-        go = tc_wait(&br.p_ready[b], (t >> 1) & 1, sh.abort, p.status) &&
-             tc_wait(C::F8 ? &br.vc_full[vs] : &br.vfull[vs], C::F8 ? (t / C::SC) & 1 : (t / C::SV) & 1, sh.abort,
-                     p.status) &&
-             (u > 0 || piece == 0 || tc_wait(br.o_free, (piece - 1) & 1, sh.abort, p.status));
-        if (go) {
-          tc::fence_after_sync();
+      tc::fence_after_sync();
+      const uint64_t vst = vd + static_cast<uint32_t>(vs * (C::TILEB >> 4));
+      if (tc_elect()) {
 #pragma unroll
-          for (int kt = 0; kt < 8; ++kt) {
-            // keys 0-63 into O_a (column 256), 64-127 into O_b (384); P's half at its S half
-            const uint32_t a = tmem + b * 128 + (kt >> 2) * 64 + (kt & 3) * 8;
-            mma_ts(tmem + 256 + (kt >> 2) * 128, a, tc::smem_desc(vbase + vs * 32768 + kt * 2048, 16384, 1024, 2),
-                   idesc128(C::F8 ? 0 : 1, 1), ((kt & 3) > 0 || u > 0) ? 1u : 0u);
-          }
-          tc::commit(C::F8 ? &br.vc_empty[vs] : &br.vempty[vs]);
-          tc::commit(&br.pv_done[b]);
+        for (int kt = 0; kt < 8; ++kt) {
+          // keys 0-63 into O_a (column 256), 64-127 into O_b (384); P's half at its S half
+          const uint32_t a = tmem + b * 128 + (kt >> 2) * 64 + (kt & 3) * 8;
+          mma_ts(tmem + 256 + (kt >> 2) * 128, a, vst + kt * 128, tc::idesc_bf16(128, 128, 0, 1),
+                 ((kt & 3) > 0 || u > 0) ? 1u : 0u);
         }
+        tc::commit(&br.vempty[vs]);
+        tc::commit(&br.pv_done[b]);
       }
-      ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+      __syncwarp();
+      ++t;
     }
     ++piece;
   }
   // every MMA has completed before the tensor memory is given back
-  if (lane == 0) {
-    tc::commit(br.idle);
-    tc_wait(br.idle, 0, sh.abort, p.status, false);
-  }
+  if (tc_elect()) tc::commit(br.idle);
   __syncwarp();
-}
-
-// ---------------------------------------------------------------- converters (e4m3)
-// 128 threads.  Thread i reads the scales of row i of a tile one tile ahead,
-// and turns eight 16-byte pieces of V's codes into f16.  The two 16-bit words
-// of four codes hold codes (0, 2) and (1, 3): V's columns 4w + {1, 2} change
-// places, and O's with them.
-template <class C>
-__device__ __forceinline__ void tc_convert(const TreeTcParams& P, unsigned char* smem) {
-  const TreeParams& p = P.t;
-  const int i = threadIdx.x - C::CONV_WARP * 32;
-  TcBars<C> br(smem);
-  const TcShared sh = shared_of<C>(smem);
-  float* scales = reinterpret_cast<float*>(smem + C::OFF_SCALE);
-  TcWalk walk(p), ahead(p);
-  TreePiece pc, apc;
-  int at = 0;  // the next tile of apc whose scales are read
-  bool amore = ahead.next(&apc);
-  if (amore) at = apc.t0;
-  int kb = 127, vb = 127;
-  auto fetch = [&]() {
-    kb = vb = 127;
-    if (!amore) return;
-    const int row = at * kRows + i;
-    RowAt ra;
-    if (row < apc.e.n && cache_row(p.cache, apc.b, row, &ra)) {
-      kb = p.cache.ks[ra.sc + apc.g * p.cache.ss_head];
-      vb = p.cache.vs[ra.sc + apc.g * p.cache.ss_head];
-    }
-    if (++at >= apc.t1) {
-      amore = ahead.next(&apc);
-      if (amore) at = apc.t0;
-    }
-  };
-  auto put = [&](int tt) {
-    float* s = scales + (tt % C::NS) * 384 + i;
-    const float nan = __uint_as_float(0x7fffffffu);
-    s[0] = kb == 255 ? nan : __uint_as_float(static_cast<uint32_t>(kb) << 23);
-    s[128] = vb == 255 ? nan : static_cast<float>(vb - 127);
-    // finite for a NaN row too: its exponent makes p NaN where it is seen, and 0 * NaN is not 0 where not
-    s[256] = vb == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(254 - vb, 1)) << 23);
-    mbar_arrive(&br.sc_full[tt % C::NS]);
-  };
-  bool more = amore;
-  if (more) {
-    fetch();
-    put(0);
-  }
-  int t = 0;
-  while (walk.next(&pc)) {
-    for (int tile = pc.t0; tile < pc.t1; ++tile, ++t) {
-      const bool next = amore;
-      fetch();
-      const int stage = t % C::SV, cs = t % C::SC;
-      if (!tc_wait_warp(&br.vfull[stage], (t / C::SV) & 1, sh.abort, p.status)) return;
-      if (t >= C::SC && !tc_wait_warp(&br.vc_empty[cs], ((t / C::SC) - 1) & 1, sh.abort, p.status)) return;
-      const unsigned char* src = smem + C::OFF_V + stage * C::TILEB;
-      unsigned char* dst = smem + C::OFF_VC + cs * 32768;
-      const int c = i & 7, r0 = i >> 3;
-      uint4 u[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4*>(src + (r0 + 16 * k) * 128 + c * 16);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = r0 + 16 * k;
-        const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t x = w[j] << 8;
-          h[2 * j] = (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
-          h[2 * j + 1] = (w[j] & 0x80008000u) | ((w[j] >> 1) & 0x3f803f80u);
-        }
-        // lanes of the two column halves store their pieces in turn, so that the
-        // eight lanes of a row write eight different banks
-        const int ch = 2 * c;
-        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-        const int sw = c >> 2;
-        *reinterpret_cast<uint4*>(dst + tile_off(r, ch + sw)) = sw ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + tile_off(r, ch + 1 - sw)) = sw ? lo : hi;
-      }
-      tc::fence_async_smem();
-      mbar_arrive(&br.vc_full[cs]);
-      // only now: given back right after the loads, the last of them was seen to
-      // bring the next tile's codes
-      mbar_arrive(&br.vempty[stage]);
-      // the scales' buffer was last read by the softmax of tile t + 1 - NS, whose PV
-      // is behind the one that vc_empty stood for
-      if (next) put(t + 1);
-    }
-  }
+  tc_wait(br.idle, 0, sh.abort, p.status, false);
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- softmax warps
 // Bits x of the result: row kb + x (x < 64) is seen by node t.
-__device__ __forceinline__ unsigned long long seen_bits(const TreeParams& p, const TreePiece& pc, int t, int kb,
-                                                        uint32_t okbox, int box_rows) {
+__device__ __noinline__ unsigned long long seen_bits(const TreeParams& p, const TreePiece& pc, int t, int kb) {
   const int first = pc.e.n - pc.e.cnt;
   const int node0 = kb - first;  // node of bit 0 (negative: rows before the draft)
   auto word = [&](int w) -> unsigned long long {
@@ -495,12 +622,83 @@ __device__ __forceinline__ unsigned long long seen_bits(const TreeParams& p, con
     v = word(w) >> s;
     if (s) v |= word(w + 1) << (64 - s);
   }
-  if (okbox != 0xffffffffu) {
-    const int r0 = kb & (kRows - 1);
-    for (int x = 0; x < 64; x += 8)  // boxes hold 8 rows or more
-      if (!((okbox >> ((r0 + x) / box_rows)) & 1u)) v &= ~(0xffull << x);
+  return v;
+}
+
+// Which rows of a key half were found, from the tile's words: 32 rows a word
+// (bf16), or a producer warp's rows 32 j + 4 w + i at bit 4 j + i (e4m3).
+template <bool F8>
+__device__ __noinline__ unsigned long long found_bits(const volatile uint32_t* okw, int hf) {
+  if (!F8) return okw[2 * hf] | (static_cast<unsigned long long>(okw[2 * hf + 1]) << 32);
+  unsigned long long v = 0;
+#pragma unroll 1
+  for (int w = 0; w < kProducers; ++w) {
+    const uint32_t m = okw[w] >> (8 * hf);
+    v |= (static_cast<unsigned long long>(m & 15u) << (4 * w)) | (static_cast<unsigned long long>((m >> 4) & 15u) << (32 + 4 * w));
   }
   return v;
+}
+
+// Half h of row r of a V tile: zeros where the row is gone; in drafted rows
+// (node >= 0) NaNs and infinities become zeros, and the node is marked.
+__device__ __noinline__ void clean_row(unsigned char* v, int r, int h, bool gone, int node, uint32_t* odd_rows) {
+  if (!gone && node < 0) return;
+  bool odd = false;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(v + tile_off(r, h * 8 + c));
+    const uint4 x = *at;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool here = gone;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
+      here |= lo | hi;
+      if (gone || lo) w[k] &= 0xffff0000u;
+      if (gone || hi) w[k] &= 0xffffu;
+    }
+    if (here) *at = make_uint4(w[0], w[1], w[2], w[3]);
+    odd |= here;
+  }
+  if (odd && !gone) atomicOr(&odd_rows[node >> 5], 1u << (node & 31));
+}
+
+// A finite code at scale byte e as the producers' bf16, infinite above its range.
+__device__ __forceinline__ float odd_e4m3(uint32_t code, int e) {
+  uint32_t a, b;
+  codes_bf16(code, &a, &b);
+  const int x = e - 127, x1 = x >> 1;
+  a = mul_bf16x2(a, static_cast<uint32_t>(127 + 60 + x - x1) << 7);
+  return __uint_as_float(mul_bf16x2(a, static_cast<uint32_t>(127 + 60 + x1) << 7) << 16);
+}
+
+// Adds the NaNs and infinities of the marked drafted rows that `node` sees to its
+// row's 64 columns from col0 on, written before by this thread.
+template <bool F8>
+__device__ __noinline__ void add_odd(const TreeParams& p, const TreePiece& pc, int node, int col0, const uint32_t* odd_rows,
+                                     uint16_t* out, float* part) {
+#pragma unroll 1
+  for (int x = 0; x < pc.e.cnt; ++x) {
+    if (!((odd_rows[x >> 5] >> (x & 31)) & 1u) || !tree_sees(p, pc.b, node, x)) continue;
+    RowAt at;
+    if (!cache_row(p.cache, pc.b, pc.e.n - pc.e.cnt + x, &at)) continue;
+    const int64_t v = at.kv + pc.g * p.cache.s_head + col0;
+#pragma unroll 1
+    for (int j = 0; j < 64; ++j) {
+      float y;
+      if (F8) {  // a NaN row, or a code whose value is above bf16's range
+        const int e = p.cache.vs[at.sc + pc.g * p.cache.ss_head];
+        y = e == 255 ? __uint_as_float(0x7fffffffu) : odd_e4m3(p.cache.v[v + j], e);
+      } else {
+        y = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.cache.v)[v + j]) << 16);
+      }
+      if (fabsf(y) < INFINITY) continue;
+      if (part)
+        part[j] += y;
+      else
+        out[j] = static_cast<uint16_t>(tc_pack(__uint_as_float(static_cast<uint32_t>(out[j]) << 16) + y, 0.f));
+    }
+  }
 }
 
 template <class C>
@@ -515,13 +713,11 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
   const TcShared sh = shared_of<C>(smem);
   const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t tl_o = tl + 256 + hf * 128;
-  const int nbox = kRows / P.t.box_rows;
-  const uint32_t all_boxes = nbox == 32 ? 0xffffffffu : (1u << nbox) - 1u;
   unsigned char* qbuf = smem + C::OFF_Q;
   // where half x of this row finds the other half's (m, l) at the end of a
   // piece: in the part of the query row that x itself writes next
   auto ml_of = [&](int x) {
-    return reinterpret_cast<float2*>(qbuf + (C::F8 ? i * 128 + (((x * 4) ^ (i & 7)) << 4) : tile_off(i, x * 8)));
+    return reinterpret_cast<float2*>(qbuf + tile_off(i, x * 8));
   };
   TcWalk walk(p);
   TreePiece pc;
@@ -532,73 +728,23 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
     const bool live = node < pc.e.cnt;
     const bool warp_live = (pc.mb * kRows + quarter * 32) / p.G < pc.e.cnt;
     const int first_draft = pc.e.n - pc.e.cnt;
-    float rowf = p.scale_log2;
     if (warp_live) {
       const unsigned char* src = p.q + 2 * (pc.b * p.q_batch + node * p.q_token + head * p.q_head);
-      if (!C::F8) {
 #pragma unroll
-        for (int c8 = 0; c8 < 8; ++c8) {
-          const int ch = hf * 8 + c8;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (live) v = *reinterpret_cast<const uint4*>(src + ch * 16);
-          *reinterpret_cast<uint4*>(qbuf + tile_off(i, ch)) = v;
-        }
-      } else {
-        uint32_t mx = 0;
-        uint4 mine[8];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (live) v = *reinterpret_cast<const uint4*>(src + (c ^ (hf * 8)) * 16);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-          if (c < 8) mine[c] = v;
-        }
-        int ex = static_cast<int>(mx >> 7);  // biased exponent of the row's largest element
-        const bool odd_q = ex == 255;        // a NaN or an infinity: the row's result is NaN
-        if (ex == 0 || odd_q) ex = 127;
-        // q * 2^-(ex - 134): the largest in [128, 256); in two factors, for the range of fp32
-        const int e1 = (ex - 134) / 2, e2 = ex - 134 - e1;
-        const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
-        const float f2 = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-        rowf = odd_q ? __uint_as_float(0x7fffffffu)
-                     : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex) << 23) * 0.0078125f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {  // 16 elements: one piece of each term
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 v = mine[2 * c + (k >> 1)];
-            const uint32_t w0 = (k & 1) ? v.z : v.x, w1 = (k & 1) ? v.w : v.y;
-            const float a[4] = {bf16lo(w0) * f1 * f2, bf16hi(w0) * f1 * f2, bf16lo(w1) * f1 * f2, bf16hi(w1) * f1 * f2};
-            hi[k] = lo[k] = 0u;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint16_t hc, lc;
-              uint32_t hh;
-              float x0, x1;
-              asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hc) : "f"(a[2 * e + 1]), "f"(a[2 * e]));
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hh) : "h"(hc));
-              asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                  : "=f"(x0), "=f"(x1)
-                  : "r"(hh));
-              asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lc) : "f"(a[2 * e + 1] - x1), "f"(a[2 * e] - x0));
-              hi[k] |= static_cast<uint32_t>(hc) << (16 * e);
-              lo[k] |= static_cast<uint32_t>(lc) << (16 * e);
-            }
-          }
-          const int ch = hf * 4 + c;
-          const uint32_t off = i * 128 + ((ch ^ (i & 7)) << 4);
-          *reinterpret_cast<uint4*>(qbuf + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(qbuf + 16384 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+      for (int c8 = 0; c8 < 8; ++c8) {
+        const int ch = hf * 8 + c8;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (live) v = *reinterpret_cast<const uint4*>(src + ch * 16);
+        if (C::F8)  // the producers' order of the columns
+          v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                         __byte_perm(v.z, v.w, 0x7632));
+        *reinterpret_cast<uint4*>(qbuf + tile_off(i, ch)) = v;
       }
       tc::fence_async_smem();
     }
     uint32_t* odd_rows = sh.odd + (piece & 1) * 8;  // last read two pieces ago
-    if (!C::F8 && threadIdx.x < 8) odd_rows[threadIdx.x] = 0u;
-    mbar_arrive(br.q_ready);
+    if (threadIdx.x < 8) odd_rows[threadIdx.x] = 0u;
+    tc_arrive_warp(br.q_ready);
 
     float m_used = NEG, lsum = 0.f;
     for (int u = pc.t0; u < pc.t1; ++u, ++t) {
@@ -606,54 +752,51 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       if (!tc_wait_warp(&br.s_ready[b], (t >> 1) & 1, sh.abort, p.status)) return;
       const int tile_row = u * kRows;
       const int kb = tile_row + hf * 64;
-      uint32_t okbox = all_boxes;
-      // written before the tile's copies were asked for; eight tiles on, this one's PV is done
-      if (p.cache.bt) okbox = *reinterpret_cast<volatile uint32_t*>(&sh.ok[t % kOkRing]);
-      const bool special = okbox != all_boxes || tile_row + kRows > first_draft;
+      bool found_all = true;
+      const volatile uint32_t* okw = sh.ok + (t % kOkRing) * 8;
+      if (p.cache.bt)  // written before the tile's rows were asked for; ten tiles on, this one's PV is done
+        found_all = (okw[0] & okw[1] & okw[2] & okw[3] &
+                     (C::F8 ? okw[4] & okw[5] & okw[6] & okw[7] : 0xffffffffu)) == 0xffffffffu;
+      const bool special = !found_all || tile_row + kRows > first_draft;
       tc::fence_after_sync();
+      unsigned long long vis = ~0ull, there = ~0ull;
+      if (__builtin_expect(special, 0)) {
+        if (!found_all) there = found_bits<C::F8>(okw, hf);
+        vis = live ? seen_bits(p, pc, node, kb) & there : 0ull;
+      }
       if (warp_live) {
-        uint32_t r[4][16];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld_32x32b_x16(tl + b * 128 + hf * 64 + c * 16, r[c]);
-        tc_wait_ld<4>(r);
-        const float* sc = nullptr;
-        if (C::F8) {
-          if (!tc_wait_warp(&br.sc_full[t % C::NS], (t / C::NS) & 1, sh.abort, p.status)) return;
-          sc = reinterpret_cast<const float*>(smem + C::OFF_SCALE) + (t % C::NS) * 384 + hf * 64;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 kf = *reinterpret_cast<const float4*>(sc + c * 16 + j);
-              const float4 ev = *reinterpret_cast<const float4*>(sc + 128 + c * 16 + j);
-              r[c][j] = __float_as_uint(fmaf(__uint_as_float(r[c][j]) * rowf, kf.x, ev.x));
-              r[c][j + 1] = __float_as_uint(fmaf(__uint_as_float(r[c][j + 1]) * rowf, kf.y, ev.y));
-              r[c][j + 2] = __float_as_uint(fmaf(__uint_as_float(r[c][j + 2]) * rowf, kf.z, ev.z));
-              r[c][j + 3] = __float_as_uint(fmaf(__uint_as_float(r[c][j + 3]) * rowf, kf.w, ev.w));
-            }
-        }
-        if (special) {
-          const unsigned long long vis =
-              live ? seen_bits(p, pc, node, kb, okbox == all_boxes ? 0xffffffffu : okbox, P.t.box_rows) : 0ull;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (!((vis >> (c * 16 + j)) & 1ull)) r[c][j] = __float_as_uint(NEG);
-        }
+        // both passes read the logits from tensor memory, 32 columns a turn: the
+        // loops stay small (all 64 in registers made the kernel's loops together
+        // larger than the SM's instruction cache)
+        const uint32_t ts = tl + b * 128 + hf * 64;
         float mraw = NEG;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[2][16];
+          tc::ld_32x32b_x16(ts + c * 32, r[0]);
+          tc::ld_32x32b_x16(ts + c * 32 + 16, r[1]);
+          tc_wait_ld<2>(r);
+          if (__builtin_expect(special, 0)) {
+            const uint32_t v = static_cast<uint32_t>(vis >> (c * 32));
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+            for (int j = 0; j < 32; ++j)
+              if (!((v >> j) & 1u)) r[j >> 4][j & 15] = __float_as_uint(NEG);
+            tc_st_x16(ts + c * 32, r[0]);
+            tc_st_x16(ts + c * 32 + 16, r[1]);
+            tc_wait_st();
+          }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) mraw = fmaxf(mraw, __uint_as_float(r[c][j]));
-        const float mx = C::F8 ? mraw : mraw * rowf;
+          for (int j = 0; j < 32; j += 2)
+            mraw = fmaxf(mraw, fmaxf(__uint_as_float(r[j >> 4][j & 15]), __uint_as_float(r[j >> 4][(j + 1) & 15])));
+        }
+        const float mx = mraw * p.scale_log2;
         const bool grow = mx > m_used + 8.f;
         const bool rescale = grow && m_used != NEG;
         if (__any_sync(FULL, rescale)) {
           if (!tc_wait_warp(&br.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, sh.abort, p.status)) return;
           tc::fence_after_sync();
           const float f = rescale ? tc_ex2(m_used - mx) : 1.f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[1][16];
             tc::ld_32x32b_x16(tl_o + c * 16, o[0]);
@@ -665,66 +808,46 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           lsum *= f;
         }
         if (grow) m_used = mx;
-        // f16's range is used from the top: p up to 2^(8 + 6)
-        const float neg = (m_used == NEG ? 0.f : -m_used) + (C::F8 ? 6.f : 0.f);
-#pragma unroll
+        const float neg = m_used == NEG ? 0.f : -m_used;
+        const f2_t neg2 = f2(neg, neg), sl2 = f2(p.scale_log2, p.scale_log2);
+        f2_t sum2 = f2(0.f, 0.f);
+#pragma unroll 1
         for (int c = 0; c < 2; ++c) {
-          uint32_t w[16];
+          uint32_t r[2][16], w[16];
+          tc::ld_32x32b_x16(ts + c * 32, r[0]);
+          tc::ld_32x32b_x16(ts + c * 32 + 16, r[1]);
+          tc_wait_ld<2>(r);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float x0 = __uint_as_float(r[2 * c + (e >> 3)][(2 * e) & 15]);
-            const float x1 = __uint_as_float(r[2 * c + (e >> 3)][(2 * e + 1) & 15]);
-            const float p0 = tc_ex2(C::F8 ? x0 + neg : fmaf(x0, rowf, neg));
-            const float p1 = tc_ex2(C::F8 ? x1 + neg : fmaf(x1, rowf, neg));
-            w[e] = tc_pack<C::F8>(p0, p1);
-            if (C::F8) {
-              const float2 iv = *reinterpret_cast<const float2*>(sc + 256 + c * 32 + 2 * e);
-              lsum = fmaf(p0, iv.x, fmaf(p1, iv.y, lsum));
-            } else {
-              lsum += p0 + p1;
-            }
+            const uint32_t* x = &r[e >> 3][(2 * e) & 15];
+            float p0, p1;
+            f2_split(f2_fma(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), sl2, neg2), &p0, &p1);
+            p0 = tc_ex2(p0);
+            p1 = tc_ex2(p1);
+            w[e] = tc_pack(p0, p1);
+            sum2 = f2_add(f2(p0, p1), sum2);
           }
-          tc_st_x16(tl + b * 128 + hf * 64 + c * 16, w);
+          // P's columns 16 c .. + 15 take the place of logits that were read
+          tc_st_x16(ts + c * 16, w);
+        }
+        {
+          float s0, s1;
+          f2_split(sum2, &s0, &s1);
+          lsum += s0 + s1;
         }
         tc_wait_st();
       }
-      if (!C::F8 && special) {
+      if (special) {
         // V's rows that the tensor core must not meet as they are
         const int stage = t % C::SV;
         if (!tc_wait_warp(&br.vfull[stage], (t / C::SV) & 1, sh.abort, p.status)) return;
-        unsigned char* v = smem + C::OFF_V + stage * C::TILEB;
-        const int r = threadIdx.x >> 1, h = threadIdx.x & 1;  // a row's half
-        const int krow = tile_row + r;
-        if (krow >= pc.e.n || !((okbox >> (r / P.t.box_rows)) & 1u)) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(v + tile_off(r, h * 8 + c)) = make_uint4(0u, 0u, 0u, 0u);
-        } else if (krow >= first_draft) {
-          bool odd = false;
-          for (int c = 0; c < 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(v + tile_off(r, h * 8 + c));
-            const uint4 x = *at;
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            bool here = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((w[k] & 0x7f80u) == 0x7f80u) {
-                w[k] &= 0xffff0000u;
-                here = true;
-              }
-              if ((w[k] & 0x7f800000u) == 0x7f800000u) {
-                w[k] &= 0xffffu;
-                here = true;
-              }
-            }
-            if (here) *at = make_uint4(w[0], w[1], w[2], w[3]);
-            odd |= here;
-          }
-          if (odd) atomicOr(&odd_rows[(krow - first_draft) >> 5], 1u << ((krow - first_draft) & 31));
-        }
+        const int r = threadIdx.x >> 1;  // two threads a row
+        const bool gone = tile_row + r >= pc.e.n || (!found_all && !((found_bits<C::F8>(okw, r >> 6) >> (r & 63)) & 1ull));
+        clean_row(smem + C::OFF_V + stage * C::TILEB, r, threadIdx.x & 1, gone, tile_row + r - first_draft, odd_rows);
         tc::fence_async_smem();
       }
       tc::fence_before_sync();
-      mbar_arrive(&br.p_ready[b]);
+      tc_arrive_warp(&br.p_ready[b]);
     }
 
     // the piece's state: both halves' outputs under one maximum
@@ -732,7 +855,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
     if (!tc_wait_warp(&br.pv_done[last & 1], (last >> 1) & 1, sh.abort, p.status)) return;
     tc::fence_after_sync();
     *ml_of(1 - hf) = make_float2(m_used, lsum);
-    mbar_arrive(br.ml_ready);
+    tc_arrive_warp(br.ml_ready);
     if (!tc_wait_warp(br.ml_ready, piece & 1, sh.abort, p.status)) return;
     if (warp_live) {
       const float2 own = make_float2(m_used, lsum), other = *ml_of(hf);
@@ -742,13 +865,12 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       const float fb = sb.x == NEG ? 1.f : tc_ex2(sb.x - M);
       const float L = fmaf(sa.y, fa, sb.y * fb);
       const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
-      const float unit = (C::F8 ? 256.f : 1.f) * (whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f);
+      const float unit = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (pc.t0 == 0 ? 1 : 0);
       float* part = p.part_o + (slot * kRows + i) * kD + hf * 64;
       unsigned char* dst = p.out + 2 * (pc.b * p.o_batch + node * p.o_token + head * p.o_head + hf * 64);
       bool odd = false;
-      if (!C::F8)
-        for (int w = 0; w < 8; ++w) odd |= odd_rows[w] != 0u;
+      for (int w = 0; w < 8; ++w) odd |= odd_rows[w] != 0u;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t ab[2][16];
@@ -758,27 +880,16 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         float o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int col = C::F8 ? (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1) : j;  // the converter's order
+          const int col = C::F8 ? (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1) : j;  // the producers' order
           o[col] = fmaf(__uint_as_float(ab[0][j]), fa, __uint_as_float(ab[1][j]) * fb) * unit;
-        }
-        if (odd && live) {
-          for (int x = 0; x < pc.e.cnt; ++x) {
-            if (!((odd_rows[x >> 5] >> (x & 31)) & 1u) || !tree_sees(p, pc.b, node, x)) continue;
-            RowAt at;
-            if (!cache_row(p.cache, pc.b, first_draft + x, &at)) continue;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.cache.v) + at.kv + pc.g * p.cache.s_head + hf * 64 + c * 16;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if ((v[j] & 0x7f80u) == 0x7f80u) o[j] += __uint_as_float(static_cast<uint32_t>(v[j]) << 16);
-          }
         }
         if (live) {
           if (whole) {
 #pragma unroll
             for (int j = 0; j < 16; j += 8)
               *reinterpret_cast<uint4*>(dst + 2 * (c * 16 + j)) =
-                  make_uint4(tc_pack<false>(o[j], o[j + 1]), tc_pack<false>(o[j + 2], o[j + 3]),
-                             tc_pack<false>(o[j + 4], o[j + 5]), tc_pack<false>(o[j + 6], o[j + 7]));
+                  make_uint4(tc_pack(o[j], o[j + 1]), tc_pack(o[j + 2], o[j + 3]),
+                             tc_pack(o[j + 4], o[j + 5]), tc_pack(o[j + 6], o[j + 7]));
           } else {
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
@@ -786,10 +897,12 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           }
         }
       }
+      if (__builtin_expect(odd, 0) && live)
+        add_odd<C::F8>(p, pc, node, hf * 64, odd_rows, reinterpret_cast<uint16_t*>(dst), whole ? nullptr : part);
       if (!whole && live && hf == 0) p.part_ml[slot * kRows + i] = make_float2(M, L);
     }
     tc::fence_before_sync();
-    mbar_arrive(br.o_free);
+    tc_arrive_warp(br.o_free);
     ++piece;
   }
 }
@@ -804,29 +917,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_tc_kernel(const __grid_con
   if (threadIdx.x == 0) {
     TcBars<C> br(smem);
     for (int s = 0; s < C::SK; ++s) {
-      mbar_init(&br.kfull[s], 1);
+      mbar_init(&br.kfull[s], C::FULL);
       mbar_init(&br.kempty[s], 1);
     }
     for (int s = 0; s < C::SV; ++s) {
-      mbar_init(&br.vfull[s], 1);
-      mbar_init(&br.vempty[s], C::F8 ? C::CONV : 1);
+      mbar_init(&br.vfull[s], C::FULL);
+      mbar_init(&br.vempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&br.s_ready[b], 1);
-      mbar_init(&br.p_ready[b], kSoft);
+      mbar_init(&br.p_ready[b], kSoft / 32);
       mbar_init(&br.pv_done[b], 1);
     }
-    mbar_init(br.q_ready, kSoft);
-    mbar_init(br.o_free, kSoft);
-    mbar_init(br.ml_ready, kSoft);
+    mbar_init(br.q_ready, kSoft / 32);
+    mbar_init(br.o_free, kSoft / 32);
+    mbar_init(br.ml_ready, kSoft / 32);
     mbar_init(br.idle, 1);
-    if (C::F8) {
-      for (int s = 0; s < C::SC; ++s) {
-        mbar_init(&br.vc_full[s], C::CONV);
-        mbar_init(&br.vc_empty[s], 1);
-      }
-      for (int s = 0; s < C::NS; ++s) mbar_init(&br.sc_full[s], C::CONV);
-    }
     *sh.abort = 0;
     fence_mbar_init();
   }
@@ -834,7 +940,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_tc_kernel(const __grid_con
     tc::tmem_alloc(sh.tmem, 512);
     tc::tmem_relinquish();
   }
-  if (threadIdx.x == C::LOAD_WARP * 32) {
+  if (!C::F8 && threadIdx.x == C::LOAD_WARP * 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmk)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tmv)) : "memory");
   }
@@ -855,10 +961,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_tc_kernel(const __grid_con
     tc_softmax<C>(P, smem, tmem);
   } else if (warp == C::MMA_WARP) {
     tc_mma<C>(P, smem, tmem);
-  } else if (warp == C::LOAD_WARP) {
-    tc_loads<C>(P, smem);
+  } else if (C::F8) {
+    tc_produce<C>(P, smem);
   } else {
-    tc_convert<C>(P, smem);
+    tc_loads<C>(P, smem);
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -885,12 +991,11 @@ EncodeTiledFn encode_fn() {
   return f;
 }
 
-// 4-D map of K or V: (d, row, head, element), or paged (d, head, row, page).
-bool encode(CUtensorMap* map, void* base, const CacheView& c, int heads, int batch, bool f8, bool swizzle,
-            int box_rows) {
+// 4-D map of a bf16 K or V: (d, row, head, element), or paged (d, head, row, page).
+bool encode(CUtensorMap* map, void* base, const CacheView& c, int heads, int batch, int box_rows) {
   const EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const int64_t es = f8 ? 1 : 2;
+  const int64_t es = 2;
   const bool paged = c.bt != nullptr;
   cuuint64_t dims[4] = {kD, static_cast<cuuint64_t>(paged ? heads : c.cap), static_cast<cuuint64_t>(paged ? c.page_rows : heads),
                         static_cast<cuuint64_t>(paged ? c.num_pages : batch)};
@@ -901,11 +1006,11 @@ bool encode(CUtensorMap* map, void* base, const CacheView& c, int heads, int bat
     if (dims[k + 1] == 1) st[k] = kD * es;
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(st[0]), static_cast<cuuint64_t>(st[1]),
                                  static_cast<cuuint64_t>(st[2])};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(f8 ? 128 : 64), 1, 1, 1};
+  cuuint32_t box[4] = {64, 1, 1, 1};
   box[paged ? 2 : 1] = static_cast<cuuint32_t>(box_rows);
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -941,11 +1046,10 @@ int tree_tc_box_rows(const CacheView& c) {
   return low < 8 ? 0 : low < kRows ? low : kRows;
 }
 
-bool tree_tc_maps(TreeTcParams* P, int cache_type) {
+bool tree_tc_maps(TreeTcParams* P) {
   const CacheView& c = P->t.cache;
-  const bool f8 = cache_type == LYC_CACHE_E4M3;
-  return encode(&P->tmk, c.k, c, P->t.Hkv, P->t.B, f8, true, P->t.box_rows) &&
-         encode(&P->tmv, c.v, c, P->t.Hkv, P->t.B, f8, !f8, P->t.box_rows);
+  return encode(&P->tmk, c.k, c, P->t.Hkv, P->t.B, P->t.box_rows) &&
+         encode(&P->tmv, c.v, c, P->t.Hkv, P->t.B, P->t.box_rows);
 }
 
 cudaError_t tree_tc_launch(const TreeTcParams* P, int cache_type, int device, cudaStream_t stream) {

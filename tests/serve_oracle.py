@@ -86,19 +86,22 @@ def sees(mask, b, t, j):
 def tree(q, cache, n, t_len, mask, scale):
     """(out, bound) [B][T][Hq][d] float64; NaN where a query is padding.
 
-    Bound: each probability carries its rounding u (fp16 or bf16) and e^delta - 1,
-    delta what fp32 does to a logit: d + 8 roundoffs of sum |q k| scale, and four of
-    the logit in log2 units (at most 1.5 times it, plus 130 for a scale's
-    exponent); over an e4m3 cache also what a query's elements lose in two e4m3 terms
-    beside the row's largest M (a power of two below it): elements under 2^-9 M are
-    off by 2^-17 M at most, the others are exact; the output its own rounding."""
+    Bound: each probability carries its rounding u and e^delta - 1.  u is bf16's:
+    bf16 rows, and e4m3 rows on the tcgen05 kernel, whose tiles are bf16, take
+    probabilities p(1 + r), |r| <= 2^-8 (8 significant bits, to nearest); the
+    mma.sync kernel's fp16 over e4m3 rows is within that (2^-11).  delta is what fp32
+    does to a logit: d + 8 roundoffs of sum |q k| scale, and four of the logit in
+    log2 units (at most 1.5 times it, plus 130 for a scale's exponent); over an e4m3
+    cache also what a query's elements lose as fp16 under the row's largest, scaled
+    to [1, 2): 8 significant bits end at fp16's last place 2^-24 for elements under
+    2^-17, which are off by half of it.  The output has its own rounding."""
     q = q.detach().cpu().double()
     B, T, Hq, d = q.shape
     G = Hq // cache.heads
     out = torch.full(q.shape, math.nan, dtype=torch.float64)
     bound = torch.zeros_like(out)
     m = None if mask is None else mask.cpu().numpy().astype(np.int64).view(np.uint64)
-    u = U16 if cache.e4m3 else UB
+    u = UB
     for b in range(B):
         nb, cnt = int(n[b]), int(t_len[b])
         if cnt <= 0 or nb < cnt:
@@ -126,7 +129,7 @@ def tree(q, cache, n, t_len, mask, scale):
             lost = 0.0
             if cache.e4m3:
                 top_q = torch.exp2(torch.floor(torch.log2(q[b, :cnt, h].abs().amax(-1, keepdim=True).clamp(min=1e-300))))
-                small = (q[b, :cnt, h].abs() < 2.0**-9 * top_q).double() * 2.0**-17 * top_q
+                small = (q[b, :cnt, h].abs() < 2.0**-17 * top_q).double() * 2.0**-25 * top_q
                 lost = (small @ k.abs().nan_to_num(posinf=0.0).T * scale).amax(-1, keepdim=True)
             delta = lost + (d + 8) * U32 * mag + 4 * U32 * (1.5 * mag + (130 if cache.e4m3 else 0)) + 8 * U32
             out[b, :cnt, h] = o
