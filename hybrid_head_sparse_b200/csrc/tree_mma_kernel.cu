@@ -636,28 +636,30 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
     c0 = static_cast<int>(sched.owner(x0));
     c1 = static_cast<int>(sched.owner(x0 + nt - 1));
   }
+  // the tcgen05 kernel's blocks of few rows: each CTA's part is in several copies
+  const int copies = ROWS == 128 ? tree_copies(e.cnt * p.G - mb * ROWS) : 1;
   pdl_wait();
   pdl_launch_dependents();
   if (c0 == c1) return;  // nothing to do, or its CTA wrote the output
   constexpr int V = D / 32;
   typedef typename std::conditional<V == 4, float4, float2>::type Part;
-  const int parts = c1 - c0 + 1;
+  const int parts = (c1 - c0 + 1) * copies;
+  // part k: copy k % copies of CTA c0 + k / copies; a group's first CTA has it in its second slot
+  auto row_of = [&](int k) {
+    const int c = c0 + k / copies;
+    return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * ROWS + (k % copies) * (ROWS / copies) + row;
+  };
   const float NEG = -INFINITY;
   float M = NEG, L = 0.f, acc[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) acc[k] = 0.f;
   for (int k0 = 0; k0 < parts; k0 += kParts) {
-    const int64_t s0 = 2 * static_cast<int64_t>(c0 + k0) * ROWS + row;
     Part u[kParts];
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-      // a group's first part lies in its CTA's second slot
-      const int64_t s = s0 + (2 * k + (k0 + k == 0 ? 1 : 0)) * static_cast<int64_t>(ROWS);
-      if (k0 + k < parts) u[k] = *reinterpret_cast<const Part*>(p.part_o + s * D + lane * V);
-    }
+    for (int k = 0; k < kParts; ++k)
+      if (k0 + k < parts) u[k] = *reinterpret_cast<const Part*>(p.part_o + row_of(k0 + k) * D + lane * V);
     float2 ml = make_float2(NEG, 0.f);
-    if (lane < kParts && k0 + lane < parts)
-      ml = p.part_ml[s0 + (2 * lane + (k0 + lane == 0 ? 1 : 0)) * static_cast<int64_t>(ROWS)];
+    if (lane < kParts && k0 + lane < parts) ml = p.part_ml[row_of(k0 + lane)];
     float m = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -16,6 +16,12 @@
 // let the QK of tile t+1 run beside the softmax of tile t.  A warp none of
 // whose rows is a query does nothing but keep the barriers going.
 //
+// A block of 64 query rows or fewer has them twice over in the 128 lanes, one of
+// 32 or fewer four times: each copy takes its half or quarter of a key half (its
+// P is zero elsewhere), so the exponentials are spread over all the schedulers
+// instead of staying with the warps of the first rows.  The copies are parts
+// like those of other CTAs, merged with them, or in the CTA for a whole group.
+//
 // bf16 rows: K and V tiles are read by the tensor core where TMA puts them.
 // Masked rows have P = 0, and 0 * NaN would reach every row, so in the tiles
 // that hold drafted rows or end an element the softmax warps clear rows past
@@ -23,9 +29,9 @@
 // that see such a row get them added at the end.
 //
 // e4m3 rows become bf16 on their way into the same tiles (code * 2^e, exact),
-// so nothing after the tiles knows the difference.  Eight producer warps find the
-// rows of coming tiles, ask L2 for them and read their scales, load 16 codes a
-// lane and instruction, convert and store them.  (Scales
+// so nothing after the tiles knows the difference.  Three warps find the rows of
+// coming tiles and their scales; eight producer warps copy the codes in, convert
+// them and store them.  (Scales
 // applied to logits and probabilities instead, K's codes as an e4m3 operand,
 // took 5000 cycles a tile against about 2000: shared memory was what it waited
 // for, with the tensor core's reads, the conversion's and the scales' on it.)
@@ -49,9 +55,13 @@ constexpr int kRows = 128;  // query rows of a block, cached rows of a tile
 constexpr int kD = 128;
 constexpr int kSoft = 256;  // softmax threads
 constexpr int kOkRing = 16;
-constexpr int kRawRing = 2;    // e4m3: tiles of codes on their way
-constexpr int kProducers = 8;  // warps
-constexpr int kUnits = 32 / kProducers;  // 4-row units of a K tile, and of a V tile, of each
+constexpr int kRawRing = 3;    // e4m3: groups of units on their way to a producer warp
+constexpr int kInfoRing = 8;   // e4m3: tiles whose rows are known
+constexpr int kProducers = 8;  // warps, half of them for K, half for V
+constexpr int kFinders = 3;    // warps that find rows, every third tile each
+constexpr int kUnits = 4;      // 4-row units that a producer warp converts at a time
+constexpr int kSide = kProducers / 2;
+constexpr int kGroups = 32 / (kSide * kUnits);  // of a warp's units of a tile
 
 template <bool F8_>
 struct TcCfg {
@@ -59,25 +69,28 @@ struct TcCfg {
   static constexpr int SK = F8 ? 2 : 3;              // K tiles
   static constexpr int SV = F8 ? 2 : 3;              // V tiles
   static constexpr int TILEB = 32768;                // a K or V tile of bf16
-  static constexpr int THREADS = 9 * 32 + (F8 ? kProducers * 32 : 32);
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9;  // F8: LOAD_WARP is the first producer
-  static constexpr int FULL = F8 ? kProducers : 1;      // arrivals that fill a tile
+  static constexpr int THREADS = 9 * 32 + (F8 ? (kFinders + kProducers) * 32 : 32);
+  static constexpr int MMA_WARP = 8, LOAD_WARP = 9;  // F8: finders from LOAD_WARP on
+  static constexpr int PROD_WARP = LOAD_WARP + kFinders;
+  static constexpr int FULL = F8 ? kProducers / 2 : 1;  // arrivals that fill a tile
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 32768;
   static constexpr int OFF_V = OFF_K + SK * TILEB;
-  static constexpr int OFF_RAW = OFF_V + SV * TILEB;  // F8: codes, [producer][kRawRing][K, V][unit][lane] of 16 bytes
-  static constexpr int OFF_BAR = OFF_RAW + (F8 ? kRawRing * 32768 : 0);
+  static constexpr int OFF_RAW = OFF_V + SV * TILEB;  // F8: codes, [producer][kRawRing][unit][lane] of 16 bytes
+  static constexpr int OFF_INFO = OFF_RAW + (F8 ? kRawRing * kProducers * kUnits * 512 : 0);  // F8: [kInfoRing][128] rows
+  static constexpr int OFF_BAR = OFF_INFO + (F8 ? kInfoRing * kRows * 16 : 0);
   // kfull, kempty [SK]; vfull, vempty [SV]; s_ready, p_ready, pv_done [2];
-  // q_ready, o_free, ml_ready, idle
-  static constexpr int NBAR = 2 * SK + 2 * SV + 6 + 4;
-  static constexpr int OFF_FLAGS = OFF_BAR + NBAR * 8;  // abort, tmem, odd rows [2][8], ok [kOkRing][8]
-  static constexpr int SMEM = OFF_FLAGS + 8 + 64 + 32 * kOkRing + 1024;  // + alignment
+  // q_ready, o_free, ml_ready, idle; F8: info_full, info_empty [kInfoRing]
+  static constexpr int NBAR = 2 * SK + 2 * SV + 6 + 4 + (F8 ? 2 * kInfoRing : 0);
+  static constexpr int OFF_FLAGS = OFF_BAR + NBAR * 8;  // abort, tmem, odd rows [2][8], ok [kOkRing][4]
+  static constexpr int SMEM = OFF_FLAGS + 8 + 64 + 16 * kOkRing + 1024;  // + alignment
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
 template <class C>
 struct TcBars {
-  uint64_t *kfull, *kempty, *vfull, *vempty, *s_ready, *p_ready, *pv_done, *q_ready, *o_free, *ml_ready, *idle;
+  uint64_t *kfull, *kempty, *vfull, *vempty, *s_ready, *p_ready, *pv_done, *q_ready, *o_free, *ml_ready, *idle,
+      *info_full, *info_empty;
   __device__ explicit TcBars(unsigned char* smem) {
     uint64_t* b = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     kfull = b;
@@ -91,6 +104,8 @@ struct TcBars {
     o_free = q_ready + 1;
     ml_ready = o_free + 1;
     idle = ml_ready + 1;
+    info_full = idle + 1;
+    info_empty = info_full + kInfoRing;
   }
 };
 
@@ -98,7 +113,7 @@ struct TcShared {
   int* abort;
   uint32_t* tmem;
   uint32_t* odd;  // [2] by piece: drafted rows with a NaN or an infinity in V, by node
-  uint32_t* ok;   // ring of the tiles' rows that were found (paged), 8 words each
+  uint32_t* ok;   // ring of the tiles' rows that were found (paged), 4 words each
 };
 template <class C>
 __device__ __forceinline__ TcShared shared_of(unsigned char* smem) {
@@ -283,7 +298,7 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
           uint32_t rows = 0;  // rows 32 lane .. + 31 by their boxes (of 8 rows or more)
           for (int x = 0; x < 32; x += 8)
             if ((found >> ((lane * 32 + x) / p.box_rows)) & 1u) rows |= 0xffu << x;
-          sh.ok[(t % kOkRing) * 8 + lane] = rows;
+          sh.ok[(t % kOkRing) * 4 + lane] = rows;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(full, bytes);
@@ -344,169 +359,197 @@ __device__ __noinline__ void convert_far(uint4 u, uint32_t e, uint4* lo, uint4* 
   *hi = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-// The rows of one producer warp, one a lane: the page of a tile's row is asked for
-// one tile before the row's place is computed and its scales are read.
-struct RowSteps {
-  const TreeParams& p;
-  TreeWalk<kRows, kRows> walk;
-  TreePiece pc;
-  bool more;
-  int tiles;         // of the run
-  int tile, row_in;  // the next tile to begin, this lane's row in a tile
-  int32_t page;
-  int64_t kv, sc;    // offsets, less the page's part
-  bool in;           // the row is one of the element's
-
-  __device__ __forceinline__ RowSteps(const TreeParams& prm, int r) : p(prm), walk(prm), tile(0), row_in(r) {
-    tiles = static_cast<int>(walk.run_tiles());
-    more = walk.next(&pc);
-    if (more) tile = pc.t0;
-    in = false;
-    page = 0;
-    kv = sc = 0;
-  }
-  __device__ __forceinline__ void begin() {
-    in = false;
-    if (!more) return;
-    const int row = tile * kRows + row_in;
-    in = row < pc.e.n;
-    kv = pc.g * p.cache.s_head;
-    sc = pc.g * p.cache.ss_head;
-    int r = row;
-    if (p.cache.bt) {
-      const int blk = page_of(p.cache, row);
-      r = row - blk * p.cache.page_rows;
-      page = p.cache.bt[in ? static_cast<int64_t>(pc.b) * p.cache.max_blocks + blk : 0];
-    } else {
-      kv += pc.b * p.cache.s_batch;
-      sc += pc.b * p.cache.ss_batch;
-    }
-    kv += r * p.cache.s_token;
-    sc += r * p.cache.ss_token;
-    if (++tile >= pc.t1) {
-      more = walk.next(&pc);
-      tile = pc.t0;
-    }
-  }
-  // The row's offset in K and V, odd where there is no such row (codes are then
-  // zeros), and its scale bytes (as they come, some row's where there is none:
-  // anything done with them here would wait for them); whether it was found.
-  __device__ __forceinline__ bool find(long long* off, uint32_t* kb, uint32_t* vb) {
-    bool have = in;
-    int64_t o = kv, at = sc;
-    if (p.cache.bt && in) {
-      have = page >= 0 && page < p.cache.num_pages;
-      if (!have && p.status) atomicOr(p.status, LYC_OP_BAD_PAGE);
-      o += page * p.cache.s_page;
-      at += page * p.cache.ss_page;
-    }
-    *off = have ? o : 1;
-    at = have ? at : 0;
-    *kb = p.cache.ks[at];
-    *vb = p.cache.vs[at];
-    return have;
-  }
+// What is known of a row of a tile.
+struct RowInfo {
+  long long off;    // of its codes in K and in V; odd: no such row, zeros
+  uint32_t factor;  // 2^(120 + e) as bf16, K's and V's << 16
+  uint32_t bytes;   // scale bytes, K's and V's << 8; bit 31: the tile has an e > 7 (or a NaN), a factor out of range
 };
 
-// Each producer warp has four 4-row units of every K tile and of every V tile,
-// eight lanes a row.  A lane copies its 16 codes of a unit to shared memory two
-// tiles ahead and converts what it copied itself, so a warp waits for nobody's
-// copies but its own.  (With the codes kept in registers instead, the loops had
-// to be unrolled over them and, with the softmax's, outgrew the SM's instruction
-// cache: 7600 cycles a tile, 40% of the instruction fetches missing.)
+// A finder warp finds the rows of every third tile of the run, lane j rows j + 32 k:
+// pages are asked for a turn ahead, and a tile's scales arrive while the next
+// one's rows are found.  A turn is a chain of some 4000 cycles, so one warp was
+// what a tile took.  (In the producers, a row a lane, it cost them 1200 cycles a
+// tile: their waits for shared memory are also waits for the loads that share a
+// counter.)
+template <class C>
+__device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* smem) {
+  const TreeParams& p = P.t;
+  const int lane = threadIdx.x & 31;
+  TcBars<C> br(smem);
+  const TcShared sh = shared_of<C>(smem);
+  RowInfo* info = reinterpret_cast<RowInfo*>(smem + C::OFF_INFO) + lane;
+  const bool paged = p.cache.bt != nullptr;
+  const int first = (threadIdx.x >> 5) - C::LOAD_WARP;
+  TcWalk walk(p);
+  TreePiece pc;
+  bool more = walk.next(&pc);
+  int tile = more ? pc.t0 : 0;
+  auto skip = [&](int n) {  // n tiles on
+    tile += n;
+    while (more && tile >= pc.t1) {
+      const int over = tile - pc.t1;
+      more = walk.next(&pc);
+      tile = pc.t0 + over;
+    }
+  };
+  skip(first);
+  int32_t page[4] = {0, 0, 0, 0};
+  uint32_t kb[4], vb[4];
+  long long off[4];
+  auto ask = [&]() {  // pages of tile `tile`
+    if (!paged || !more) return;
+    const int64_t row_of = static_cast<int64_t>(pc.b) * p.cache.max_blocks;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = tile * kRows + lane + 32 * k;
+      page[k] = p.cache.bt[row_of + page_of(p.cache, min(row, pc.e.n - 1))];
+    }
+  };
+  auto put = [&](int t) {
+    bool far = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (off[k] & 1) kb[k] = vb[k] = 127u;
+      far |= kb[k] > 134u || vb[k] > 134u;
+    }
+    const uint32_t flag = __any_sync(0xffffffffu, far) ? 0x80000000u : 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<uint4*>(&info[(t % kInfoRing) * kRows + 32 * k]) =
+          make_uint4(static_cast<uint32_t>(off[k]), static_cast<uint32_t>(off[k] >> 32),
+                     ((kb[k] + 120u) << 7) | ((vb[k] + 120u) << 23), kb[k] | (vb[k] << 8) | flag);
+    tc_arrive_warp(&br.info_full[t % kInfoRing]);
+  };
+  ask();
+  int t = first;
+#pragma unroll 1
+  for (; more; t += kFinders) {
+    if (t >= kFinders) put(t - kFinders);
+    if (t >= kInfoRing && !tc_wait_warp(&br.info_empty[t % kInfoRing], ((t / kInfoRing) - 1) & 1, sh.abort, p.status))
+      return;
+    const int64_t kv0 = pc.g * p.cache.s_head + (paged ? 0 : pc.b * p.cache.s_batch);
+    const int64_t sc0 = pc.g * p.cache.ss_head + (paged ? 0 : pc.b * p.cache.ss_batch);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = tile * kRows + lane + 32 * k;
+      bool have = row < pc.e.n;
+      int r = row;
+      int64_t at = sc0;
+      off[k] = kv0;
+      if (paged) {
+        r = row - page_of(p.cache, row) * p.cache.page_rows;
+        const bool in = page[k] >= 0 && page[k] < p.cache.num_pages;
+        if (have && !in && p.status) atomicOr(p.status, LYC_OP_BAD_PAGE);
+        have = have && in;
+        off[k] += page[k] * p.cache.s_page;
+        at += page[k] * p.cache.ss_page;
+        const uint32_t found = __ballot_sync(0xffffffffu, have);
+        if (lane == k) sh.ok[(t % kOkRing) * 4 + k] = found;
+      }
+      off[k] = have ? off[k] + r * p.cache.s_token : 1;
+      at = have ? at + r * p.cache.ss_token : 0;
+      kb[k] = p.cache.ks[at];  // some row's where there is none
+      vb[k] = p.cache.vs[at];
+    }
+    skip(kFinders);
+    ask();
+  }
+  if (t >= kFinders) put(t - kFinders);
+}
+
+// Half of the producer warps have K, half V; a warp has every kSide-th 4-row unit
+// of a tile, eight lanes a row.  A lane copies its 16 codes of a unit to shared
+// memory kRawRing groups ahead and converts what it copied itself, so a warp waits for
+// nobody's copies but its own.  (With the codes kept in registers instead, the
+// loops had to be unrolled over them and, with the softmax's, outgrew the SM's
+// instruction cache: 7600 cycles a tile, 40% of the instruction fetches missing.)
 template <class C>
 __device__ __forceinline__ void tc_produce(const TreeTcParams& P, unsigned char* smem) {
   const TreeParams& p = P.t;
-  const int w = (threadIdx.x >> 5) - C::LOAD_WARP, lane = threadIdx.x & 31;
+  const int pw = (threadIdx.x >> 5) - C::PROD_WARP, lane = threadIdx.x & 31;
+  const int w = pw % kSide, kv = pw / kSide;
   // eight adjacent lanes store half a row each of an even and an odd row: with
   // the swizzle, eight different banks
   const int c = (lane & 3) | (((lane >> 3) & 1) << 2);
-  const int rr = ((lane >> 4) << 1) | ((lane >> 2) & 1);
-  const int r0 = w * 4 + rr;  // the first unit's row; + 32 for each unit
+  const int r0 = w * 4 + (((lane >> 4) << 1) | ((lane >> 2) & 1));  // the first unit's row; + 4 kSide for each unit
   TcBars<C> br(smem);
   const TcShared sh = shared_of<C>(smem);
+  uint64_t* const full = kv ? br.vfull : br.kfull;
+  uint64_t* const empty = kv ? br.vempty : br.kempty;
+  const int S = kv ? C::SV : C::SK;
+  unsigned char* const tiles = smem + (kv ? C::OFF_V : C::OFF_K);
+  const unsigned char* const base = (kv ? p.cache.v : p.cache.k) + c * 16;
+  const uint32_t sel = kv ? 0x3232u : 0x1010u;
   const uint32_t st0 = tile_off(r0, 2 * c), st1 = tile_off(r0, 2 * c + 1);
-  constexpr int HALFB = kUnits * 512;  // a warp's codes of a K or V tile
-  unsigned char* const raw = smem + C::OFF_RAW + w * (kRawRing * 2 * HALFB) + lane * 16;
-  const unsigned char* const kg = p.cache.k + c * 16;
-  const unsigned char* const vg = p.cache.v + c * 16;
-  // lanes l and l + 16 look after row 32 (l / 4) + 4 w + l % 4: unit l / 4
-  RowSteps st(p, ((lane >> 2) & 3) * 32 + w * 4 + (lane & 3));
-  const int ntile = st.tiles;
-  if (ntile == 0) return;
-  long long off;
-  uint32_t s0 = 0, s1 = 0;     // scale bytes (K's, V's << 8) of this tile's row and the next one's
-  uint32_t kb = 127, vb = 127;  // and those of the one after, on their way
-  bool have = false;
-  // the rows that were found, a word for this warp's 32 rows of a tile
-  auto find = [&](int t) {
-    have = st.find(&off, &kb, &vb);
-    const uint32_t m = __ballot_sync(0xffffffffu, have);
-    if (p.cache.bt && lane == 0) sh.ok[(t % kOkRing) * 8 + w] = m;
-    st.begin();
-  };
-  auto copy = [&](int t) {  // with the offsets just found
-    if (t >= 0 && t < ntile) {
-      const uint32_t dst = smem_u32(raw + (t % kRawRing) * 2 * HALFB);
-#pragma unroll
-      for (int j = 0; j < kUnits; ++j) {
-        const long long o = __shfl_sync(0xffffffffu, off, 4 * j + rr);
-        const int n = (o & 1) ? 0 : 16;
-        const long long at = o & ~1ll;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 512), "l"(kg + at), "r"(n) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + HALFB + j * 512), "l"(vg + at), "r"(n)
-                     : "memory");
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  st.begin();
+  unsigned char* const raw = smem + C::OFF_RAW + pw * (kRawRing * kUnits * 512) + lane * 16;
+  const RowInfo* const info = reinterpret_cast<const RowInfo*>(smem + C::OFF_INFO) + r0;
+  const uint2 run = tree_run<kRows, kRows>(p);
+  const int groups = kGroups * static_cast<int>(run.y - run.x);
 #pragma unroll 1
-  for (int t = -3; t < ntile; ++t) {  // tile t is converted, t + 2 copied, t + 3 found
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRawRing - 1) : "memory");
-    const bool far = __any_sync(0xffffffffu, ((s0 & 255u) > 134u) || ((s0 >> 8) > 134u));
-#pragma unroll 1
-    for (int kv = 0; kv < 2 && t >= 0; ++kv) {
-      const int S = kv ? C::SV : C::SK, stage = t % S;
-      if (t >= S && !tc_wait_warp((kv ? br.vempty : br.kempty) + stage, ((t / S) - 1) & 1, sh.abort, p.status)) {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        return;
-      }
-      const unsigned char* src = raw + (t % kRawRing) * 2 * HALFB + kv * HALFB;
-      unsigned char* dst = smem + (kv ? C::OFF_V : C::OFF_K) + stage * C::TILEB;
-      const uint32_t mine = (kv ? s0 >> 8 : s0) & 255u;
-      if (__builtin_expect(far, 0)) {
+  for (int h = -kRawRing; h < groups; ++h) {  // group h is converted, h + kRawRing copied
+    if (h >= 0) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRawRing - 1) : "memory");
+      const int t = h / kGroups, g = h % kGroups, stage = t % S;
+      if (g == 0 && t >= S && !tc_wait_warp(empty + stage, ((t / S) - 1) & 1, sh.abort, p.status)) break;
+      const unsigned char* src = raw + (h % kRawRing) * (kUnits * 512);
+      const RowInfo* rows = info + (t % kInfoRing) * kRows + g * (kRows / kGroups);
+      unsigned char* dst = tiles + stage * C::TILEB + g * (kRows / kGroups) * 128;
+      if (__builtin_expect(rows->bytes >> 31, 0)) {
 #pragma unroll 1
         for (int j = 0; j < kUnits; ++j) {
           uint4 lo, hi;
-          convert_far(*reinterpret_cast<const uint4*>(src + j * 512), __shfl_sync(0xffffffffu, mine, 4 * j + rr), &lo, &hi);
-          *reinterpret_cast<uint4*>(dst + st0 + j * 4096) = lo;
-          *reinterpret_cast<uint4*>(dst + st1 + j * 4096) = hi;
+          convert_far(*reinterpret_cast<const uint4*>(src + j * 512), (rows[4 * kSide * j].bytes >> (8 * kv)) & 255u, &lo, &hi);
+          *reinterpret_cast<uint4*>(dst + st0 + j * (kSide * 512)) = lo;
+          *reinterpret_cast<uint4*>(dst + st1 + j * (kSide * 512)) = hi;
         }
       } else {
-        const uint32_t factor = ((mine + 120u) << 7) * 0x10001u;  // 2^(120 + e - 127) twice
+        // (all loads before the first store: the compiler cannot tell them apart, and
+        // one unit after another ran at 200 cycles a unit)
+        uint4 codes[kUnits];
+        uint32_t factor[kUnits];
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
-          const uint4 u = *reinterpret_cast<const uint4*>(src + j * 512);
-          const uint32_t f = __shfl_sync(0xffffffffu, factor, 4 * j + rr);
-          uint32_t h[8];
-          codes_bf16(u.x, &h[0], &h[1]);
-          codes_bf16(u.y, &h[2], &h[3]);
-          codes_bf16(u.z, &h[4], &h[5]);
-          codes_bf16(u.w, &h[6], &h[7]);
+          codes[j] = *reinterpret_cast<const uint4*>(src + j * 512);
+          factor[j] = rows[4 * kSide * j].factor;
+        }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f);
-          *reinterpret_cast<uint4*>(dst + st0 + j * 4096) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + st1 + j * 4096) = make_uint4(h[4], h[5], h[6], h[7]);
+        for (int j = 0; j < kUnits; ++j) {
+          const uint4 u = codes[j];
+          const uint32_t f = __byte_perm(factor[j], 0, sel);
+          uint32_t x[8];
+          codes_bf16(u.x, &x[0], &x[1]);
+          codes_bf16(u.y, &x[2], &x[3]);
+          codes_bf16(u.z, &x[4], &x[5]);
+          codes_bf16(u.w, &x[6], &x[7]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = mul_bf16x2(x[k], f);
+          *reinterpret_cast<uint4*>(dst + st0 + j * (kSide * 512)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(dst + st1 + j * (kSide * 512)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
       }
-      tc::fence_async_smem();
-      tc_arrive_warp((kv ? br.vfull : br.kfull) + stage);
+      if (g == kGroups - 1) {
+        tc::fence_async_smem();
+        tc_arrive_warp(full + stage);
+        if (lane == 0) mbar_arrive(&br.info_empty[t % kInfoRing]);
+      }
     }
-    s0 = s1;
-    s1 = have ? kb | (vb << 8) : 127u | (127u << 8);
-    copy(t + 2);
-    find(t + 3);
+    const int hn = h + kRawRing;
+    if (hn < groups) {
+      const int t = hn / kGroups, g = hn % kGroups;
+      if (g == 0 && !tc_wait_warp(&br.info_full[t % kInfoRing], (t / kInfoRing) & 1, sh.abort, p.status)) break;
+      const RowInfo* rows = info + (t % kInfoRing) * kRows + g * (kRows / kGroups);
+      const uint32_t dst = smem_u32(raw + (hn % kRawRing) * (kUnits * 512));
+      long long off[kUnits];
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j) off[j] = rows[4 * kSide * j].off;
+#pragma unroll
+      for (int j = 0; j < kUnits; ++j)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + j * 512), "l"(base + (off[j] & ~1ll)),
+                     "r"((off[j] & 1) ? 0 : 16)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -625,20 +668,6 @@ __device__ __noinline__ unsigned long long seen_bits(const TreeParams& p, const 
   return v;
 }
 
-// Which rows of a key half were found, from the tile's words: 32 rows a word
-// (bf16), or a producer warp's rows 32 j + 4 w + i at bit 4 j + i (e4m3).
-template <bool F8>
-__device__ __noinline__ unsigned long long found_bits(const volatile uint32_t* okw, int hf) {
-  if (!F8) return okw[2 * hf] | (static_cast<unsigned long long>(okw[2 * hf + 1]) << 32);
-  unsigned long long v = 0;
-#pragma unroll 1
-  for (int w = 0; w < kProducers; ++w) {
-    const uint32_t m = okw[w] >> (8 * hf);
-    v |= (static_cast<unsigned long long>(m & 15u) << (4 * w)) | (static_cast<unsigned long long>((m >> 4) & 15u) << (32 + 4 * w));
-  }
-  return v;
-}
-
 // Half h of row r of a V tile: zeros where the row is gone; in drafted rows
 // (node >= 0) NaNs and infinities become zeros, and the node is marked.
 __device__ __noinline__ void clean_row(unsigned char* v, int r, int h, bool gone, int node, uint32_t* odd_rows) {
@@ -701,6 +730,86 @@ __device__ __noinline__ void add_odd(const TreeParams& p, const TreePiece& pc, i
   }
 }
 
+// The copies of a whole group's rows merged into its output, by all softmax warps
+// (half hf has columns 64 hf .. + 63), 32 columns a turn through the query
+// buffer.  (M, L) is the copy's state, fa and fb its key halves' factors.
+struct CopyMerge {
+  uint32_t tl;  // this warp's lanes of the tensor memory
+  int hf, copy, copies, li, span;
+  bool live;
+  float M, L, fa, fb;
+  unsigned char* qbuf;
+  uint64_t* bar;  // all softmax warps'
+  int* abort;
+  uint32_t* status;
+  unsigned char* dst;
+};
+template <class C>
+__device__ __noinline__ bool merge_copies(const CopyMerge& m, uint32_t phase) {
+  float2* cm = reinterpret_cast<float2*>(m.qbuf + 24576);
+  auto together = [&]() {
+    tc_arrive_warp(m.bar);
+    return tc_wait_warp(m.bar, phase++ & 1, m.abort, m.status);
+  };
+  if (!together()) return false;  // the halves' states have been read
+  if (m.hf == 0) cm[m.copy * m.span + m.li] = make_float2(m.M, m.L);
+#pragma unroll 1
+  for (int step = 0; step < 2; ++step) {
+    uint32_t a[2][16], b[2][16];
+    const uint32_t col = m.tl + 256 + m.hf * 64 + step * 32;
+    tc::ld_32x32b_x16(col, a[0]);
+    tc::ld_32x32b_x16(col + 16, a[1]);
+    tc::ld_32x32b_x16(col + 128, b[0]);
+    tc::ld_32x32b_x16(col + 144, b[1]);
+    tc_wait_ld<2>(a);
+    tc_wait_ld<2>(b);
+    float o[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int to = C::F8 ? (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1) : j;  // the producers' order
+      o[to] = fmaf(__uint_as_float(a[j >> 4][j & 15]), m.fa, __uint_as_float(b[j >> 4][j & 15]) * m.fb);
+    }
+    unsigned char* mine = m.qbuf + m.li * 256 + m.hf * 128;
+    if (m.copy > 0)
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<float4*>(mine + (m.copy - 1) * m.span * 256 + ((q ^ (m.li & 7)) << 4)) =
+            make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    if (!together()) return false;
+    if (m.copy == 0 && m.live) {
+      float M = m.M;
+      for (int k = 1; k < m.copies; ++k) M = fmaxf(M, cm[k * m.span + m.li].x);
+      const float f0 = m.M == -INFINITY ? 1.f : tc_ex2(m.M - M);  // 1: the state is zero, or NaN
+      float L = m.L * f0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] *= f0;
+#pragma unroll 1
+      for (int k = 1; k < m.copies; ++k) {
+        const float2 s = cm[k * m.span + m.li];
+        const float f = s.x == -INFINITY ? 1.f : tc_ex2(s.x - M);
+        L = fmaf(s.y, f, L);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float4 u = *reinterpret_cast<const float4*>(mine + (k - 1) * m.span * 256 + ((q ^ (m.li & 7)) << 4));
+          o[4 * q] = fmaf(u.x, f, o[4 * q]);
+          o[4 * q + 1] = fmaf(u.y, f, o[4 * q + 1]);
+          o[4 * q + 2] = fmaf(u.z, f, o[4 * q + 2]);
+          o[4 * q + 3] = fmaf(u.w, f, o[4 * q + 3]);
+        }
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(m.dst + step * 64 + q * 16) =
+            make_uint4(tc_pack(o[8 * q] * inv, o[8 * q + 1] * inv), tc_pack(o[8 * q + 2] * inv, o[8 * q + 3] * inv),
+                       tc_pack(o[8 * q + 4] * inv, o[8 * q + 5] * inv), tc_pack(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
+    }
+    if (!together()) return false;
+  }
+  return true;
+}
+constexpr uint32_t kMergeWaits = 5;
+
 template <class C>
 __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char* smem, uint32_t tmem) {
   const TreeParams& p = P.t;
@@ -722,11 +831,15 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
   TcWalk walk(p);
   TreePiece pc;
   int t = 0, piece = 0;
+  uint32_t together = 0;  // times that all softmax warps have waited for one another
   while (walk.next(&pc)) {
-    const int row = pc.mb * kRows + i;
+    const int copies = tree_copies(pc.e.cnt * p.G - pc.mb * kRows), span = kRows / copies;
+    const int copy = i / span;
+    const int row = pc.mb * kRows + i - copy * span;
     const int node = row / p.G, head = pc.g * p.G + row % p.G;
     const bool live = node < pc.e.cnt;
-    const bool warp_live = (pc.mb * kRows + quarter * 32) / p.G < pc.e.cnt;
+    const bool warp_live = (pc.mb * kRows + (quarter * 32) % span) / p.G < pc.e.cnt;
+    const int k0 = copy * (64 / copies);  // the copy's keys of the half: k0 .. k0 + 64 / copies - 1
     const int first_draft = pc.e.n - pc.e.cnt;
     if (warp_live) {
       const unsigned char* src = p.q + 2 * (pc.b * p.q_batch + node * p.q_token + head * p.q_head);
@@ -753,41 +866,55 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       const int tile_row = u * kRows;
       const int kb = tile_row + hf * 64;
       bool found_all = true;
-      const volatile uint32_t* okw = sh.ok + (t % kOkRing) * 8;
+      const volatile uint32_t* okw = sh.ok + (t % kOkRing) * 4;
       if (p.cache.bt)  // written before the tile's rows were asked for; ten tiles on, this one's PV is done
-        found_all = (okw[0] & okw[1] & okw[2] & okw[3] &
-                     (C::F8 ? okw[4] & okw[5] & okw[6] & okw[7] : 0xffffffffu)) == 0xffffffffu;
+        found_all = (okw[0] & okw[1] & okw[2] & okw[3]) == 0xffffffffu;
       const bool special = !found_all || tile_row + kRows > first_draft;
       tc::fence_after_sync();
       unsigned long long vis = ~0ull, there = ~0ull;
       if (__builtin_expect(special, 0)) {
-        if (!found_all) there = found_bits<C::F8>(okw, hf);
+        if (!found_all) there = okw[2 * hf] | (static_cast<unsigned long long>(okw[2 * hf + 1]) << 32);
         vis = live ? seen_bits(p, pc, node, kb) & there : 0ull;
       }
       if (warp_live) {
         // both passes read the logits from tensor memory, 32 columns a turn: the
         // loops stay small (all 64 in registers made the kernel's loops together
-        // larger than the SM's instruction cache)
+        // larger than the SM's instruction cache); a quarter's 16 stay in registers
         const uint32_t ts = tl + b * 128 + hf * 64;
         float mraw = NEG;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[2][16];
-          tc::ld_32x32b_x16(ts + c * 32, r[0]);
-          tc::ld_32x32b_x16(ts + c * 32 + 16, r[1]);
-          tc_wait_ld<2>(r);
+        uint32_t few[1][16];
+        if (copies == 4) {
+          tc::ld_32x32b_x16(ts + k0, few[0]);
+          tc_wait_ld<1>(few);
           if (__builtin_expect(special, 0)) {
-            const uint32_t v = static_cast<uint32_t>(vis >> (c * 32));
+            const uint32_t v = static_cast<uint32_t>(vis >> k0);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((v >> j) & 1u)) r[j >> 4][j & 15] = __float_as_uint(NEG);
-            tc_st_x16(ts + c * 32, r[0]);
-            tc_st_x16(ts + c * 32 + 16, r[1]);
-            tc_wait_st();
+            for (int j = 0; j < 16; ++j)
+              if (!((v >> j) & 1u)) few[0][j] = __float_as_uint(NEG);
           }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2)
-            mraw = fmaxf(mraw, fmaxf(__uint_as_float(r[j >> 4][j & 15]), __uint_as_float(r[j >> 4][(j + 1) & 15])));
+          for (int j = 0; j < 16; j += 2)
+            mraw = fmaxf(mraw, fmaxf(__uint_as_float(few[0][j]), __uint_as_float(few[0][j + 1])));
+        } else {
+#pragma unroll 1
+          for (int c = k0; c < k0 + 64 / copies; c += 32) {
+            uint32_t r[2][16];
+            tc::ld_32x32b_x16(ts + c, r[0]);
+            tc::ld_32x32b_x16(ts + c + 16, r[1]);
+            tc_wait_ld<2>(r);
+            if (__builtin_expect(special, 0)) {
+              const uint32_t v = static_cast<uint32_t>(vis >> c);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((v >> j) & 1u)) r[j >> 4][j & 15] = __float_as_uint(NEG);
+              tc_st_x16(ts + c, r[0]);
+              tc_st_x16(ts + c + 16, r[1]);
+              tc_wait_st();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              mraw = fmaxf(mraw, fmaxf(__uint_as_float(r[j >> 4][j & 15]), __uint_as_float(r[j >> 4][(j + 1) & 15])));
+          }
         }
         const float mx = mraw * p.scale_log2;
         const bool grow = mx > m_used + 8.f;
@@ -811,24 +938,42 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         const float neg = m_used == NEG ? 0.f : -m_used;
         const f2_t neg2 = f2(neg, neg), sl2 = f2(p.scale_log2, p.scale_log2);
         f2_t sum2 = f2(0.f, 0.f);
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[2][16], w[16];
-          tc::ld_32x32b_x16(ts + c * 32, r[0]);
-          tc::ld_32x32b_x16(ts + c * 32 + 16, r[1]);
-          tc_wait_ld<2>(r);
+        auto prob = [&](const uint32_t* x) -> uint32_t {  // two columns' probabilities, packed
+          float p0, p1;
+          f2_split(f2_fma(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), sl2, neg2), &p0, &p1);
+          p0 = tc_ex2(p0);
+          p1 = tc_ex2(p1);
+          sum2 = f2_add(f2(p0, p1), sum2);
+          return tc_pack(p0, p1);
+        };
+        // P's columns (two keys each) take the place of logits that were read
+        if (copies == 4) {
+          uint32_t w[2][16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const uint32_t* x = &r[e >> 3][(2 * e) & 15];
-            float p0, p1;
-            f2_split(f2_fma(f2(__uint_as_float(x[0]), __uint_as_float(x[1])), sl2, neg2), &p0, &p1);
-            p0 = tc_ex2(p0);
-            p1 = tc_ex2(p1);
-            w[e] = tc_pack(p0, p1);
-            sum2 = f2_add(f2(p0, p1), sum2);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t x = prob(&few[0][2 * e]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q >> 1][(q & 1) * 8 + e] = copy == q ? x : 0u;
           }
-          // P's columns 16 c .. + 15 take the place of logits that were read
-          tc_st_x16(ts + c * 16, w);
+          tc_st_x16(ts, w[0]);
+          tc_st_x16(ts + 16, w[1]);
+        } else {
+          uint32_t w[16];
+#pragma unroll 1
+          for (int c = k0; c < k0 + 64 / copies; c += 32) {
+            uint32_t r[2][16];
+            tc::ld_32x32b_x16(ts + c, r[0]);
+            tc::ld_32x32b_x16(ts + c + 16, r[1]);
+            tc_wait_ld<2>(r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = prob(&r[e >> 3][(2 * e) & 15]);
+            tc_st_x16(ts + c / 2, w);
+          }
+          if (copies == 2) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = 0u;
+            tc_st_x16(ts + 16 * (1 - copy), w);
+          }
         }
         {
           float s0, s1;
@@ -842,7 +987,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         const int stage = t % C::SV;
         if (!tc_wait_warp(&br.vfull[stage], (t / C::SV) & 1, sh.abort, p.status)) return;
         const int r = threadIdx.x >> 1;  // two threads a row
-        const bool gone = tile_row + r >= pc.e.n || (!found_all && !((found_bits<C::F8>(okw, r >> 6) >> (r & 63)) & 1ull));
+        const bool gone = tile_row + r >= pc.e.n || (!found_all && !((okw[r >> 5] >> (r & 31)) & 1u));
         clean_row(smem + C::OFF_V + stage * C::TILEB, r, threadIdx.x & 1, gone, tile_row + r - first_draft, odd_rows);
         tc::fence_async_smem();
       }
@@ -856,21 +1001,27 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
     tc::fence_after_sync();
     *ml_of(1 - hf) = make_float2(m_used, lsum);
     tc_arrive_warp(br.ml_ready);
-    if (!tc_wait_warp(br.ml_ready, piece & 1, sh.abort, p.status)) return;
-    if (warp_live) {
+    if (!tc_wait_warp(br.ml_ready, together++ & 1, sh.abort, p.status)) return;
+    const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
+    const bool merge = whole && copies > 1;
+    if (warp_live || merge) {
       const float2 own = make_float2(m_used, lsum), other = *ml_of(hf);
       const float2 sa = hf ? other : own, sb = hf ? own : other;
       const float M = fmaxf(sa.x, sb.x);
       const float fa = sa.x == NEG ? 1.f : tc_ex2(sa.x - M);  // 1: the state is zero, or NaN
       const float fb = sb.x == NEG ? 1.f : tc_ex2(sb.x - M);
       const float L = fmaf(sa.y, fa, sb.y * fb);
-      const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
       const float unit = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (pc.t0 == 0 ? 1 : 0);
       float* part = p.part_o + (slot * kRows + i) * kD + hf * 64;
       unsigned char* dst = p.out + 2 * (pc.b * p.o_batch + node * p.o_token + head * p.o_head + hf * 64);
       bool odd = false;
       for (int w = 0; w < 8; ++w) odd |= odd_rows[w] != 0u;
+      if (merge) {
+        const CopyMerge cm{tl, hf, copy, copies, i - copy * span, span, live, M, L, fa, fb, qbuf, br.ml_ready, sh.abort, p.status, dst};
+        if (!merge_copies<C>(cm, together)) return;
+        together += kMergeWaits;
+      } else
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t ab[2][16];
@@ -897,7 +1048,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           }
         }
       }
-      if (__builtin_expect(odd, 0) && live)
+      if (__builtin_expect(odd, 0) && live && copy == 0)
         add_odd<C::F8>(p, pc, node, hf * 64, odd_rows, reinterpret_cast<uint16_t*>(dst), whole ? nullptr : part);
       if (!whole && live && hf == 0) p.part_ml[slot * kRows + i] = make_float2(M, L);
     }
@@ -933,6 +1084,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_tc_kernel(const __grid_con
     mbar_init(br.o_free, kSoft / 32);
     mbar_init(br.ml_ready, kSoft / 32);
     mbar_init(br.idle, 1);
+    if (C::F8)
+      for (int s = 0; s < kInfoRing; ++s) {
+        mbar_init(&br.info_full[s], 1);
+        mbar_init(&br.info_empty[s], kProducers);
+      }
     *sh.abort = 0;
     fence_mbar_init();
   }
@@ -961,10 +1117,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_tc_kernel(const __grid_con
     tc_softmax<C>(P, smem, tmem);
   } else if (warp == C::MMA_WARP) {
     tc_mma<C>(P, smem, tmem);
-  } else if (C::F8) {
-    tc_produce<C>(P, smem);
-  } else {
+  } else if (!C::F8) {
     tc_loads<C>(P, smem);
+  } else if (warp < C::PROD_WARP) {
+    tc_rows<C>(P, smem);
+  } else {
+    tc_produce<C>(P, smem);
   }
   tc::fence_before_sync();
   __syncthreads();
