@@ -146,6 +146,13 @@ int sm_count(int device) {
   return sms;
 }
 
+// The tcgen05 kernel has query blocks of 128 rows, the mma.sync kernel of 16 or 32.
+// Its blocks read the cache again, so above 32 rows it loses: 36 rows over 131072
+// cached rows (32/8 heads, us) mma.sync 193 bf16 and 262 e4m3, tcgen05 92 and 116;
+// over 2048 rows 16.0 and 16.0 to 15.8 and 20.5.  Within 32 rows the longest caches
+// would gain and the others lose (32 rows over 131072: 99 and 134 to 97 and 120;
+// over 2048: 14 and 15 to 20 and 25; 16 elements of 1024: 35 and 32 to 36 and 44),
+// and a capacity says little of the lengths.
 constexpr int kMmaMostRows = 32;
 
 struct TreeShape {

@@ -131,9 +131,10 @@ __device__ __forceinline__ uint32_t codes02(uint32_t w) { return codes13(w << 8)
 
 __device__ __forceinline__ uint16_t bf16_bits(const unsigned char* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
-// The loads of one warp's chunks: where each row lies is looked up one chunk
-// ahead of its copies, its scale bytes are kept in registers for one chunk
-// before they go to shared memory.
+// The loads of one warp's chunks: where the rows lie is looked up one chunk
+// ahead of its copies, their scale bytes are kept in registers for one chunk
+// before they go to shared memory.  Where a chunk never spans two pages, it is
+// looked up as a whole and its rows are a stride apart; else each row is.
 template <class C>
 struct TmLoader {
   const TreeParams& p;
@@ -146,12 +147,13 @@ struct TmLoader {
   unsigned long long ok;  // rows of the looked-up chunk that exist
   int kb[C::KPL], vb[C::KPL];  // scale bytes waiting for shared memory
   int pending;                 // their stage, or -1
+  const bool whole;            // a chunk is within one page
 
   __device__ __forceinline__ TmLoader(const TreeParams& prm, const TreePiece& piece, unsigned char* smem, int w, int l)
       : p(prm), pc(piece), ring(smem + w * C::WARPB),
         scales(reinterpret_cast<float*>(smem + C::OFF_SC + w * C::ST * C::SCB)),
         okw(reinterpret_cast<unsigned long long*>(smem + C::OFF_OK) + w * C::ST), warp(w), lane(l),
-        nchunks(piece.t1 - piece.t0), pending(-1) {}
+        nchunks(piece.t1 - piece.t0), pending(-1), whole(!prm.cache.bt || prm.cache.page_rows % C::KC == 0) {}
 
   __device__ __forceinline__ int first_row(int i) const { return (pc.t0 + i) * C::TR + warp * C::KC; }
 
@@ -159,6 +161,15 @@ struct TmLoader {
     ok = 0;
     if (i >= nchunks) return;
     const int base = first_row(i);
+    if (whole) {
+      const int rows = min(C::KC, pc.e.n - base);
+      if (rows <= 0) return;
+      if (cache_row(p.cache, pc.b, base, &at[0]))
+        ok = ~0ull >> (64 - rows);
+      else if (lane == 0 && p.status)
+        atomicOr(p.status, LYC_OP_BAD_PAGE);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < C::KPL; ++k) {
       const int r = k * 32 + lane;
@@ -198,14 +209,29 @@ struct TmLoader {
       const int ch = lane % C::LPR;
       const unsigned char* kg = p.cache.k + pc.g * p.cache.s_head * (C::F8 ? 1 : 2) + ch * 16;
       const unsigned char* vg = p.cache.v + pc.g * p.cache.s_head * (C::F8 ? 1 : 2) + ch * 16;
+      if (whole) {
+        const int64_t step = p.cache.s_token * (C::F8 ? C::RPI : 2 * C::RPI);
+        int64_t off = ok ? at[0].kv * (C::F8 ? 1 : 2) + (lane / C::LPR) * (step / C::RPI) : 0;
+        const int rows = __popcll(ok) - lane / C::LPR;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const int r = s * C::RPI + lane / C::LPR;
-        const int64_t kv = __shfl_sync(0xffffffffu, at[(s * C::RPI) / 32].kv, r & 31);
-        const bool have = (ok >> r) & 1ull;
-        const int64_t off = have ? kv * (C::F8 ? 1 : 2) : 0;
-        cp16(smem_u32(k + k_off<C>(r, ch)), kg + off, have ? 16 : 0);
-        cp16(smem_u32(k + 4096 + v_off<C>(r, ch)), vg + off, have ? 16 : 0);
+        for (int s = 0; s < 8; ++s) {
+          const int r = s * C::RPI + lane / C::LPR;
+          const bool have = s * C::RPI < rows;
+          const int64_t o = have ? off : 0;
+          cp16(smem_u32(k + k_off<C>(r, ch)), kg + o, have ? 16 : 0);
+          cp16(smem_u32(k + 4096 + v_off<C>(r, ch)), vg + o, have ? 16 : 0);
+          off += step;
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const int r = s * C::RPI + lane / C::LPR;
+          const int64_t kv = __shfl_sync(0xffffffffu, at[(s * C::RPI) / 32].kv, r & 31);
+          const bool have = (ok >> r) & 1ull;
+          const int64_t off = have ? kv * (C::F8 ? 1 : 2) : 0;
+          cp16(smem_u32(k + k_off<C>(r, ch)), kg + off, have ? 16 : 0);
+          cp16(smem_u32(k + 4096 + v_off<C>(r, ch)), vg + off, have ? 16 : 0);
+        }
       }
       if (lane == 0) okw[stage] = ok;
       if (C::F8) {
@@ -214,8 +240,9 @@ struct TmLoader {
           const int r = j * 32 + lane;
           kb[j] = vb[j] = 127;
           if (r < C::KC && ((ok >> r) & 1ull)) {
-            kb[j] = p.cache.ks[at[j].sc + pc.g * p.cache.ss_head];
-            vb[j] = p.cache.vs[at[j].sc + pc.g * p.cache.ss_head];
+            const int64_t sc = (whole ? at[0].sc + r * p.cache.ss_token : at[j].sc) + pc.g * p.cache.ss_head;
+            kb[j] = p.cache.ks[sc];
+            vb[j] = p.cache.vs[sc];
           }
         }
         pending = stage;
