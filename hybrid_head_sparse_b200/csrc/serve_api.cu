@@ -91,9 +91,12 @@ lyc_status check_cache(const lyc_layer_cache* c, bool writes) {
     return refuse(LYC_ERR_INVALID_ARG, "token and head strides must be at least head_dim");
   if (writes && c->block_table == nullptr && c->batch > 1 && c->s_batch < c->head_dim)
     return refuse(LYC_ERR_INVALID_ARG, "a cache that is written needs a batch stride of its own");
+  if (writes && c->block_table && c->num_pages > 1 && c->s_page < c->head_dim)
+    return refuse(LYC_ERR_INVALID_ARG, "a cache that is written needs a page stride of its own");
   if (f8 && (c->ss_batch < 0 || c->ss_head < 0 || c->ss_token < 0 || c->ss_page < 0))
     return refuse(LYC_ERR_INVALID_ARG, "negative scale stride");
-  if (f8 && writes && ((per > 1 && c->ss_token < 1) || (c->num_kv_heads > 1 && c->ss_head < 1)))
+  if (f8 && writes && ((per > 1 && c->ss_token < 1) || (c->num_kv_heads > 1 && c->ss_head < 1) ||
+                       (c->block_table ? c->num_pages > 1 && c->ss_page < 1 : c->batch > 1 && c->ss_batch < 1)))
     return refuse(LYC_ERR_INVALID_ARG, "scales that are written need strides of their own");
   return LYC_OK;
 }

@@ -572,6 +572,253 @@ def test_offsets_past_32_bits(lyc):
     check_tree(lyc, small, q, [700])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,hq,cap,page", [
+    (3, 4, 90, 0), (12, 8, 90, 16), (12, 8, 400, 16), (60, 8, 300, 0), (33, 2, 520, 8),
+])
+def test_tree_many_elements(lyc, e4m3, T, hq, cap, page):
+    """More elements than a warp has lanes, most of them short: several whole
+    groups a CTA, caches of one tile, blocks of few rows beside full ones."""
+    B, hkv = 41, 2
+    rng = np.random.default_rng(cap + T)
+    cap = -(-cap // page) * page if page else cap
+    t_len = [int(x) for x in rng.integers(0, T + 1, B)]
+    n = [int(rng.integers(c, cap + 1)) for c in t_len]
+    t_len[7], n[7], t_len[40], n[40] = T, cap, T, T
+    cache = fill(lyc, B, hkv, 128, cap, page, e4m3, seed=cap)
+    poison_past(cache, n)
+    q = randn(T, B, T, hq, 128)
+    mask = random_tree(rng, B, T)
+    check_tree(lyc, cache, q, n, t_len, mask, what="many")
+
+
+@pytest.mark.parametrize("T,page", [(3, 0), (3, 16), (20, 0), (20, 16)])
+def test_tree_scales_of_every_size(lyc, T, page):
+    """Scales far from 1 in K and V: V's to 2^23 apart over few query rows (fp16
+    probabilities times scales hold 2^30), to 2^120 over many."""
+    cap, n = 320, [310, 131]
+    cache = fill(lyc, 2, 1, 128, cap, page, True, seed=12)
+    k, v, ks, vs, _ = cache.tensors
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    # codes of 1 .. 7 times 2^-9 with a scale of 2^9 or 2^10: keys of ordinary size
+    small = torch.randint(1, 8, k.shape, generator=g, device="cuda", dtype=torch.uint8)
+    sign = torch.randint(0, 2, k.shape, generator=g, device="cuda", dtype=torch.uint8) << 7
+    k.view(torch.uint8).copy_(small | sign)
+    ks.view(torch.uint8).copy_(torch.randint(136, 138, ks.shape, generator=g, device="cuda", dtype=torch.uint8))
+    v.view(torch.uint8).copy_(small.flip(0) + 0x30 | sign)  # no zeros: 1.0 .. 1.875 / 2
+    choice = torch.tensor([127, 134, 135, 150] if T * 4 <= 32 else [30, 127, 135, 150], dtype=torch.uint8, device="cuda")
+    vs.view(torch.uint8).copy_(choice[torch.randint(0, 4, vs.shape, generator=g, device="cuda")])
+    q = randn(7, 2, T, 4, 128, scale=0.3)
+    check_tree(lyc, cache, q, n, None, None, what="scales")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T", [4, 20])
+def test_tree_cache_orders(lyc, e4m3, T):
+    """The same rows in other orders and with padding between them: rows before
+    heads, pages with heads outermost, scales of a page row by row and unaligned,
+    one prefix shared by all elements."""
+    B, hkv, d, cap, page = 3, 2, 128, 400, 16
+    n = [400, 77, T]
+    q = randn(5, B, T, 8, d)
+    mask = random_tree(np.random.default_rng(T), B, T)
+    base = fill(lyc, B, hkv, d, cap, 0, e4m3, seed=21)
+    k, v, ks, vs, _ = base.tensors
+    want = check_tree(lyc, base, q, n, None, mask, what="plain")
+    es, by = (torch.uint8, torch.uint8) if e4m3 else (BF, None)
+
+    def wide(x, shape, perm):
+        """x copied into a tensor of order `perm` whose rows are 16 elements longer"""
+        x = x.view(es) if e4m3 else x
+        y = torch.zeros([shape[p] for p in perm] + [d + 16], dtype=es, device="cuda")
+        y = y.permute([perm.index(i) for i in range(3)] + [3])[..., :d]
+        y.copy_(x)
+        return y.view(k.dtype) if e4m3 else y
+
+    def apart(s, perm, pad):
+        if s is None:
+            return None
+        s = s.view(torch.uint8)
+        y = torch.zeros([s.shape[p] for p in perm[:2]] + [s.shape[perm[2]] + pad], dtype=torch.uint8, device="cuda")
+        y = y[..., 1: s.shape[perm[2]] + 1].permute([perm.index(i) for i in range(3)])  # starts at an odd byte
+        y.copy_(s)
+        return y
+
+    for perm in ([0, 2, 1], [2, 1, 0], [1, 0, 2]):
+        c = lyc.KvCache(wide(k, k.shape, perm), wide(v, v.shape, perm), apart(ks, perm, 5), apart(vs, perm, 5))
+        out, st = run_tree(lyc, c, q, n, None, mask)
+        assert st == 0 and torch.equal(out, want), perm
+    # pages
+    rng = np.random.default_rng(2)
+    bt, pages = block_table(rng, B, cap // page)
+    idx = bt.long().flatten()
+
+    def paged(x, shape):
+        y = torch.zeros((pages, page, hkv) + shape, dtype=x.dtype, device="cuda")
+        y[idx] = x.transpose(1, 2).unflatten(1, (cap // page, page)).flatten(0, 1)
+        return y
+
+    def as_bytes(x):
+        return x.view(torch.uint8) if e4m3 else x
+
+    pk, pv = (paged(as_bytes(x), (d,)) for x in (k, v))
+    ps = [paged(s.view(torch.uint8), ()) if e4m3 else None for s in (ks, vs)]
+    for perm in ([0, 1, 2], [0, 2, 1], [2, 0, 1], [1, 2, 0]):
+        c = lyc.KvCache(wide(pk, pk.shape, perm), wide(pv, pv.shape, perm), apart(ps[0], perm, 3), apart(ps[1], perm, 3),
+                        block_table=bt)
+        out, st = run_tree(lyc, c, q, n, None, mask)
+        assert st == 0 and torch.equal(out, want), perm
+    # every element reads element 0's rows
+    one = [None if x is None else as_bytes(x)[:1].expand(x.shape) for x in (k, v)]
+    two = [None if s is None else s.view(torch.uint8)[:1].expand(s.shape) for s in (ks, vs)]
+    c = lyc.KvCache(one[0].view(k.dtype) if e4m3 else one[0], one[1].view(k.dtype) if e4m3 else one[1], *two)
+    check_tree(lyc, c, q, n, None, mask, what="shared prefix")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_tree_pages_too_small_for_a_tile(lyc, e4m3):
+    """Pages of 4 and 6 rows under many query rows: blocks of 32 rows of the kernel
+    that looks up every row."""
+    for page in (4, 6):
+        n = [150, 40]
+        cache = fill(lyc, 2, 1, 128, 156, page, e4m3, seed=page)
+        poison_past(cache, n)
+        check_tree(lyc, cache, randn(3, 2, 17, 4, 128), n, None, random_tree(np.random.default_rng(1), 2, 17), what="small pages")
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T", [2, 24])
+def test_tree_two_calls_at_once(lyc, e4m3, T):
+    """Two eager calls on two streams over one cache, each with a workspace of its
+    own that held anything, and one that is too small or is not aligned."""
+    cache = fill(lyc, 2, 2, 128, 6000, 64, e4m3, seed=30)
+    qs = [randn(i, 2, T, 8, 128) for i in range(2)]
+    lens = [[6000, 500], [900, 5999]]
+    want = [run_tree(lyc, cache, qs[i], lens[i])[0] for i in range(2)]
+    need = lyc.tree_workspace_bytes(cache, T, 8)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.zeros_like(want[0]) for _ in range(2)]
+    ns = [i32(x) for x in lens]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            lyc.tree_attention(qs[i], cache, ns[i], outs[i], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], want[i])
+    for bad in (ws[0][: need - 1], ws[0].new_empty(need + 16)[8: need + 8]):
+        with pytest.raises(lyc.LycError):
+            lyc.tree_attention(qs[0], cache, ns[0], outs[0], workspace=bad)
+
+
+def test_captured_step_follows_its_lengths(lyc):
+    """Norm, append, attention and read captured once; replayed with lengths,
+    positions and tokens changed on the device, it does each step's work."""
+    B, hq, hkv, d = 2, 8, 2, 128
+    bt, pages = block_table(np.random.default_rng(3), B, 12)
+    make = lambda: lyc.KvCache.empty(B, hkv, d, page_rows=16, num_pages=pages, block_table=bt)  # noqa: E731
+    a, b = make(), make()
+    freq, w = inv_freq(d), (1 + randn(1, d, scale=0.1).float()).to(BF)
+    q, k, v = randn(2, B, 1, hq, d), randn(3, B, 1, hkv, d), randn(4, B, 1, hkv, d)
+    n, pos = i32([1, 1]), i32([0, 0])
+    qo, out, kn = torch.empty_like(q), torch.empty_like(q), torch.empty_like(k[:, 0])
+    ko = torch.zeros((B, hkv, 8, d), dtype=torch.float32, device="cuda")
+    vo = torch.zeros_like(ko)
+
+    def step(cache, qo, out, kn, ko, vo):
+        lyc.qk_norm_rope(None, k[:, 0], pos, freq, None, kn, k_weight=w)
+        lyc.cache_append(cache, n, k, v, q=q, q_out=qo, inv_freq=freq, q_weight=w, k_weight=w)
+        lyc.tree_attention(qo, cache, n, out)
+        lyc.cache_read(cache, n, ko, vo)
+
+    step(a, qo, out, kn, ko, vo)  # outside a capture first
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(a, qo, out, kn, ko, vo)
+    mine = [torch.empty_like(qo), torch.empty_like(out), torch.empty_like(kn), torch.zeros_like(ko), torch.zeros_like(vo)]
+    step(b, *mine)
+    for i in range(1, 150):
+        q.copy_(randn(100 + i, *q.shape))
+        k.copy_(randn(300 + i, *k.shape))
+        n.copy_(i32([i + 1, i // 2 + 1]))
+        pos.copy_(n - 1)
+        g.replay()
+        step(b, *mine)
+        if i % 37 == 0 or i == 149:
+            torch.cuda.synchronize()
+            for x, y in zip((qo, out, kn, ko, vo), mine):
+                assert torch.equal(x, y), i
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a.tensors[:4], b.tensors[:4]))
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_norm_rope_many_heads_and_rows(lyc, dtype):
+    """More than 256 rows of heads that are many times and no multiple of what a
+    block takes at once, in place."""
+    rows, hq, hkv, d = 300, 41, 11, 128
+    q, k = randn(1, rows, hq, d, dtype=dtype), randn(2, rows, hkv, d, dtype=dtype)
+    pos = torch.arange(rows, device="cuda", dtype=torch.int32) * 977
+    freq, w = inv_freq(64), (1 + randn(3, d, scale=0.2).float()).to(dtype)
+    qo, ko = q.clone(), k.clone()
+    lyc.qk_norm_rope(qo, ko, pos, freq, qo, ko, w, w, interleaved=False)
+    u = SO.UB if dtype == BF else SO.U32
+    for got, x in ((qo, q), (ko, k)):
+        y, slack = SO.norm_rope(x, w, pos, freq, False, 1e-6)
+        SO.close(got, y, y.abs() * u + slack * (1 + u), "many heads")
+
+
+def test_append_many_tokens(lyc):
+    """A prompt of more than 256 tokens of many heads: the bytes that the same
+    tokens give one at a time."""
+    B, T, hq, hkv, d = 1, 300, 20, 9, 64
+    freq, w = inv_freq(d), (1 + randn(1, d, scale=0.1).float()).to(BF)
+    q, k, v = randn(2, B, T, hq, d), randn(3, B, T, hkv, d), randn(4, B, T, hkv, d)
+    a, b = (lyc.KvCache.empty(B, hkv, d, rows=310) for _ in range(2))
+    qa, qb = torch.empty_like(q), torch.empty_like(q)
+    lyc.cache_append(a, i32([T]), k, v, q=q, q_out=qa, inv_freq=freq, q_weight=w, k_weight=w)
+    for t in range(T):
+        s = slice(t, t + 1)
+        lyc.cache_append(b, i32([t + 1]), k[:, s], v[:, s], q=q[:, s], q_out=qb[:, s], inv_freq=freq, q_weight=w, k_weight=w)
+    assert torch.equal(qa, qb)
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a.tensors[:4], b.tensors[:4]))
+
+
+def test_wrappers_refuse_what_does_not_fit(lyc):
+    """Wrong types, shapes, orders and devices are refused before anything runs."""
+    cache = lyc.KvCache.empty(2, 2, 64, rows=32)
+    q, k = randn(1, 2, 3, 4, 64), randn(2, 2, 3, 2, 64)
+    n, out = i32([5, 5]), torch.empty((2, 3, 4, 64), dtype=BF, device="cuda")
+    bad = [
+        lambda: lyc.tree_attention(q.float(), cache, n, out),
+        lambda: lyc.tree_attention(q[:1], cache, n, out),
+        lambda: lyc.tree_attention(q.transpose(2, 3).contiguous().transpose(2, 3), cache, n, out),
+        lambda: lyc.tree_attention(q, cache, n.long(), out),
+        lambda: lyc.tree_attention(q, cache, n.cpu(), out),
+        lambda: lyc.tree_attention(q, cache, n[:1], out),
+        lambda: lyc.tree_attention(q, cache, n, out, mask=torch.zeros((2, 3), dtype=torch.int64, device="cuda")),
+        lambda: lyc.tree_attention(q, cache, n, out[..., :32]),
+        lambda: lyc.tree_attention(q, cache, n, out, status=torch.zeros(1, device="cuda")),
+        lambda: lyc.tree_attention(randn(1, 2, 257, 4, 64), cache, n, torch.empty((2, 257, 4, 64), dtype=BF, device="cuda")),
+        lambda: lyc.cache_append(cache, n, k, k.float()),
+        lambda: lyc.cache_append(cache, n, k[:, :, :1], k[:, :, :1]),
+        lambda: lyc.cache_append(cache, n, k, k, q=q),
+        lambda: lyc.cache_append(cache, n, k, k, inv_freq=inv_freq(64).double()),
+        lambda: lyc.cache_read(cache, n, k.transpose(1, 2).half(), k.transpose(1, 2)),
+        lambda: lyc.cache_read(cache, n, k, k),
+        lambda: lyc.qk_norm_rope(q[0], k[0], None, inv_freq(64), q[0], k[0]),
+        lambda: lyc.qk_norm_rope(q[0], k[0].float(), i32([0, 1, 2]), inv_freq(64), q[0], k[0]),
+        lambda: lyc.qk_norm_rope(q[0], None, i32([0, 1]), inv_freq(64), q[0], None),
+        lambda: lyc.KvCache(cache.tensors[0], cache.tensors[1]),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(lyc.LycError):
+            call()
+            pytest.fail(f"call {i} was taken")
+
+
 # ------------------------------------------------------------------ together
 
 

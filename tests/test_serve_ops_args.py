@@ -175,3 +175,11 @@ def test_wrapper_refuses_tensors_off_the_gpu(lyc):
     q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
     with pytest.raises(lyc.LycError):
         lyc.qk_norm_rope(q, None, torch.zeros(2, dtype=torch.int32), torch.ones(32), q, None)
+
+
+def test_pages_and_scales_that_are_written_lie_apart(lyc):
+    for kw in (dict(s_page=0), dict(s_page=64), dict(ss_page=0)):
+        assert lyc.lyc_cache_append(paged(lyc, **kw), append(lyc), None) == -1
+        assert "of its own" in lyc.lyc_operator_error() or "of their own" in lyc.lyc_operator_error()
+    assert lyc.lyc_cache_append(cache(lyc, ss_batch=0), append(lyc), None) == -1
+    assert lyc.lyc_cache_read(paged(lyc, s_page=0, ss_page=0), read(lyc, m=0), None) == 0
