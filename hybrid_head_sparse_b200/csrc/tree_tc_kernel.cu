@@ -12,8 +12,8 @@
 // end of a run.  P overwrites S in tensor memory (16-bit, half the columns)
 // and is the A operand from there, so it costs no shared memory and no shared
 // memory bandwidth, and the ring of K/V tiles is as deep as the SM allows.
-// Warp 8 issues the MMAs (one thread), warp 9 the TMA copies; two S buffers
-// let the QK of tile t+1 run beside the softmax of tile t.  A warp none of
+// Warp 8 issues the MMAs (one thread), for bf16 rows warp 9 the TMA copies; two
+// S buffers let the QK of tile t+1 run beside the softmax of tile t.  A warp none of
 // whose rows is a query does nothing but keep the barriers going.
 //
 // A block of 64 query rows or fewer has them twice over in the 128 lanes, one of
@@ -33,8 +33,17 @@
 // coming tiles and their scales; eight producer warps copy the codes in, convert
 // them and store them.  (Scales
 // applied to logits and probabilities instead, K's codes as an e4m3 operand,
-// took 5000 cycles a tile against about 2000: shared memory was what it waited
-// for, with the tensor core's reads, the conversion's and the scales' on it.)
+// took 212 us where this takes 175: the scales cost every logit two operations.
+// Codes brought by TMA and scales by warps of their own took 205.)
+//
+// Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 92 to
+// 98 us, 5.5 to 5.8 TB/s, 0.84 to 0.89 of the copy rate: HBM, and the
+// exponentials (1024 cycles of a tile's 2600).  4 x 16 nodes over up to 65536
+// e4m3 rows each: 175 us, 0.35 of the floor.  There a tile takes 3300 cycles
+// against the 1300 of its bytes: the conversion is 36 instructions for 16 codes,
+// most of them on a pipe of half rate (900 cycles a scheduler), shared memory 1800,
+// and what is left are each role's chains of latencies, with twenty warps an SM
+// to cover them.  2 x 64 nodes over up to 32768 rows: 111 to 130 us, the same.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
