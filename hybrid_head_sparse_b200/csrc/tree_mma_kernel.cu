@@ -17,8 +17,8 @@
 // floor at the copy rate), 4 x 8192 rows 30 (0.68), 4097 rows 9.6 with the merge
 // (2.6 of bytes; the rest is the chain length, page, rows, states, merge).
 //
-// 8-bit rows: codes become f16 by moving bits (value * 2^-8, exact), so both
-// products run in f16 with fp32 sums.  Which elements share a register is
+// 8-bit rows: codes become f16, exactly, so both products run in f16 with fp32
+// sums.  Which elements share a register is
 // free in a sum over the head's dimensions, so K's codes are read 16 bytes at
 // a time in an order that needs no shuffling and Q is laid out to match.  A
 // query row is scaled by a power of two to below 2 before it becomes f16
@@ -128,11 +128,13 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// e4m3 codes in bytes 1 and 3 (0 and 2) as f16 of value * 2^-8: the sign stays,
-// the four exponent and three mantissa bits move to the low end of f16's
-// exponent and the top of its mantissa.
-__device__ __forceinline__ uint32_t codes13(uint32_t w) { return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u); }
-__device__ __forceinline__ uint32_t codes02(uint32_t w) { return codes13(w << 8); }
+// Four e4m3 codes as f16, exactly: codes 0 and 1, codes 2 and 3.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* h01, uint32_t* h23) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(*h01), "=r"(*h23)
+      : "r"(w));
+}
 
 __device__ __forceinline__ uint16_t bf16_bits(const unsigned char* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
               qa[mt][ks][hf + 2 * e] =
                   live ? *reinterpret_cast<const uint32_t*>(src + 2 * (ks * 16 + e * 8 + j4 * 2)) : 0u;
         } else {
-          // dims 64 blk + 16 j4 + 4 s + {0, 2} and {1, 3} of step 4 blk + s
+          // dims 64 blk + 16 j4 + 4 s + {0, 1} and {2, 3} of step 4 blk + s
           uint32_t raw[D / 64][8];
           uint32_t mx = 0;
 #pragma unroll
@@ -337,15 +339,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
           const int e1 = (ex - 127) / 2, e2 = ex - 127 - e1;
           const float f1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
           const float f2 = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-          // K's codes are read as value * 2^-8
-          rowf[mt][hf] = p.scale_log2 * 256.f * __uint_as_float(static_cast<uint32_t>(ex) << 23);
+          rowf[mt][hf] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex) << 23);
 #pragma unroll
           for (int blk = 0; blk < D / 64; ++blk)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               const uint32_t w0 = raw[blk][2 * s], w1 = raw[blk][2 * s + 1];
-              qa[mt][blk * 4 + s][hf] = pack16<true>(bf16lo(w0) * f1 * f2, bf16lo(w1) * f1 * f2);
-              qa[mt][blk * 4 + s][hf + 2] = pack16<true>(bf16hi(w0) * f1 * f2, bf16hi(w1) * f1 * f2);
+              qa[mt][blk * 4 + s][hf] = pack16<true>(bf16lo(w0) * f1 * f2, bf16hi(w0) * f1 * f2);
+              qa[mt][blk * 4 + s][hf + 2] = pack16<true>(bf16lo(w1) * f1 * f2, bf16hi(w1) * f1 * f2);
             }
         }
       }
@@ -407,7 +408,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
               const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
               for (int st = 0; st < 4; ++st) {
-                const uint32_t b0 = codes02(w[st]), b1 = codes13(w[st]);
+                uint32_t b0, b1;
+                codes_f16(w[st], &b0, &b1);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) mma16<true>(s[mt][t], qa[mt][blk * 4 + st], b0, b1);
               }
@@ -542,6 +544,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             __syncwarp();
           }
         }
+        if (C::F8 && key0 + 16 > first_draft) {
+          // a drafted row that some queries do not see and nobody has written yet may
+          // hold any byte: the NaN codes, which a written row never has, become zeros
+          for (int e = lane; e < 16 * (D / 16); e += 32) {
+            uint4* at = reinterpret_cast<uint4*>(vbuf + v_off<C>(sub * 16 + e / (D / 16), e % (D / 16)));
+            const uint4 u = *at;
+            uint32_t w[4] = {u.x, u.y, u.z, u.w}, any = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = (((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;  // 1 in such a byte
+              any |= nan;
+              w[k] &= ~(nan * 255u);
+            }
+            if (any) *at = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+        }
         if (!C::F8) {
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
@@ -560,8 +579,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             ldsm4t(vf, smem_u32(vbuf + v_off<C>(sub * 16 + (lane & 15), dt * 2 + (lane >> 4))));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const uint32_t e0 = codes02(vf[2 * half]), e1 = codes02(vf[2 * half + 1]);
-              const uint32_t o0 = codes13(vf[2 * half]), o1 = codes13(vf[2 * half + 1]);
+              // two keys' codes of an even and an odd dim lie alternately
+              uint32_t e0, e1, o0, o1;
+              codes_f16(__byte_perm(vf[2 * half], 0u, 0x3120), &e0, &o0);
+              codes_f16(__byte_perm(vf[2 * half + 1], 0u, 0x3120), &e1, &o1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 mma16<true>(o[mt][4 * dt + 2 * half], pa[mt], e0, e1);
@@ -598,12 +619,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             *reinterpret_cast<float2*>(ow + row * D + n * 8 + 2 * j4) =
                 make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
         } else {
-          // V's codes were read as value * 2^-8; tiles 2c and 2c + 1 hold the even and odd dims
+          // tiles 2c and 2c + 1 hold the even and odd dims
 #pragma unroll
           for (int c = 0; c < D / 16; ++c)
             *reinterpret_cast<float4*>(ow + row * D + c * 16 + 4 * j4) =
-                make_float4(o[mt][2 * c][2 * hf] * 256.f, o[mt][2 * c + 1][2 * hf] * 256.f,
-                            o[mt][2 * c][2 * hf + 1] * 256.f, o[mt][2 * c + 1][2 * hf + 1] * 256.f);
+                make_float4(o[mt][2 * c][2 * hf], o[mt][2 * c + 1][2 * hf], o[mt][2 * c][2 * hf + 1],
+                            o[mt][2 * c + 1][2 * hf + 1]);
         }
       }
     __syncthreads();
