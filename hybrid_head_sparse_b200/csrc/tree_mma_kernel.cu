@@ -25,9 +25,10 @@
 // (exact for elements down to 2^-14 of the row's largest).  V's scales 2^e_j
 // go into the exponent: p'_j = 2^(z_j + e_j - m'), m' the running maximum of
 // z_j + e_j, so p' stays in f16's range whatever the scales are, and the sum
-// takes p'_j 2^-e_j.  One token over 131072 such rows: 74 us, 0.56 of the floor,
-// bound by instructions: 576 a warp for 16 rows, of which the codes' moves are
-// 224 on the pipe of half rate.  (12 warps of half the chunk: 78; 16 spill.)
+// takes p'_j 2^-e_j.  One token over 131072 such rows: 61 us, 0.67 of the floor (8192 x 4:
+// 24, 0.43; head_dim 64: 48), bound by instructions and their chains: codes
+// converted by bit moves took 74, 16 rows at a time 66 (32 at a time cost a cache
+// of 300 rows 1 us of 18), 12 warps of half the chunk no less.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -54,6 +55,8 @@ struct TmCfg {
   static constexpr int ROWB = D * (F8 ? 1 : 2);
   static constexpr int KC = 4096 / ROWB;        // rows of a warp's chunk
   static constexpr int TR = NW * KC;            // rows of a tile
+  static constexpr int SUB = F8 && MT == 1 ? 32 : 16;  // rows a warp takes at a time
+  static constexpr int KT = SUB / 8;
   static constexpr int LPR = ROWB / 16;         // 16-byte pieces of a row
   static constexpr int RPI = 32 / LPR;          // rows of one warp-wide copy
   static constexpr int KPL = (KC + 31) / 32;    // rows a lane looks up
@@ -378,14 +381,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
       const float* sc = ld.scales + stage * (C::KC * 3);
 
 #pragma unroll 1
-      for (int sub = 0; sub < C::KC / 16; ++sub) {
-        const int key0 = base + sub * 16;
+      for (int sub = 0; sub < C::KC / C::SUB; ++sub) {
+        const int key0 = base + sub * C::SUB;
         if (key0 >= pc.e.n) break;
-        float s[MT][2][4];
+        float s[MT][C::KT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < C::KT; ++t)
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[mt][t][c] = 0.f;
         if (!C::F8) {
@@ -401,10 +404,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
           }
         } else {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < C::KT; ++t)
 #pragma unroll
             for (int blk = 0; blk < D / 64; ++blk) {
-              const uint4 u = *reinterpret_cast<const uint4*>(kbuf + k_off<C>(sub * 16 + t * 8 + g4, blk * 4 + j4));
+              const uint4 u = *reinterpret_cast<const uint4*>(kbuf + k_off<C>(sub * C::SUB + t * 8 + g4, blk * 4 + j4));
               const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
               for (int st = 0; st < 4; ++st) {
@@ -416,11 +419,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             }
         }
         // log2-unit logits, with V's exponent where rows are scaled
-        float isv[2][2];
+        float isv[C::KT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < C::KT; ++t) {
           if (C::F8) {
-            const int k = sub * 16 + t * 8 + 2 * j4;
+            const int k = sub * C::SUB + t * 8 + 2 * j4;
             const float2 kf = *reinterpret_cast<const float2*>(sc + k);
             const float2 ev = *reinterpret_cast<const float2*>(sc + C::KC + k);
             const float2 iv = *reinterpret_cast<const float2*>(sc + 2 * C::KC + k);
@@ -438,8 +441,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
               for (int c = 0; c < 4; ++c) s[mt][t][c] *= rowf[mt][c >> 1];
           }
         }
-        const uint32_t okh = static_cast<uint32_t>(ok >> (sub * 16)) & 0xffffu;
-        const bool masked = okh != 0xffffu || key0 + 16 > first_draft;
+        constexpr uint32_t kAll = 0xffffffffu >> (32 - C::SUB);
+        const uint32_t okh = static_cast<uint32_t>(ok >> (sub * C::SUB)) & kAll;
+        const bool masked = okh != kAll || key0 + C::SUB > first_draft;
         if (masked) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -447,7 +451,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             for (int c = 0; c < 4; ++c) {
               const int t = (pc.mb * C::ROWS + mt * 16 + (c >> 1) * 8 + g4) / p.G;
 #pragma unroll
-              for (int tl = 0; tl < 2; ++tl) {
+              for (int tl = 0; tl < C::KT; ++tl) {
                 const int kk = tl * 8 + 2 * j4 + (c & 1);
                 const int node = key0 + kk - first_draft;
                 const bool sees = ((okh >> kk) & 1u) &&
@@ -463,7 +467,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            mx[mt][hf] = fmaxf(fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]), fmaxf(s[mt][1][2 * hf], s[mt][1][2 * hf + 1]));
+            mx[mt][hf] = fmaxf(s[mt][0][2 * hf], s[mt][0][2 * hf + 1]);
+#pragma unroll
+            for (int t = 1; t < C::KT; ++t)
+              mx[mt][hf] = fmaxf(mx[mt][hf], fmaxf(s[mt][t][2 * hf], s[mt][t][2 * hf + 1]));
             grow |= mx[mt][hf] > m[mt][hf] + 8.f;
           }
         if (__any_sync(FULL, grow)) {
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
               }
             }
         }
-        uint32_t pa[MT][4];
+        uint32_t pa[MT][C::SUB / 16][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -494,13 +501,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             // f16's range is used from the top: p' up to 2^(8 + 6)
             const float neg = (m[mt][hf] == NEG ? 0.f : -m[mt][hf]) + (C::F8 ? 6.f : 0.f);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int t = 0; t < C::KT; ++t) {
               const float p0 = ex2(s[mt][t][2 * hf] + neg), p1 = ex2(s[mt][t][2 * hf + 1] + neg);
               if (C::F8)
                 l[mt][hf] = fmaf(p0, isv[t][0], fmaf(p1, isv[t][1], l[mt][hf]));
               else
                 l[mt][hf] += p0 + p1;
-              pa[mt][hf + 2 * t] = pack16<C::F8>(p0, p1);
+              pa[mt][t >> 1][hf + 2 * (t & 1)] = pack16<C::F8>(p0, p1);
             }
           }
         if (!C::F8 && key0 + 16 > first_draft) {
@@ -544,11 +551,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             __syncwarp();
           }
         }
-        if (C::F8 && key0 + 16 > first_draft) {
+        if (C::F8 && key0 + C::SUB > first_draft) {
           // a drafted row that some queries do not see and nobody has written yet may
           // hold any byte: the NaN codes, which a written row never has, become zeros
-          for (int e = lane; e < 16 * (D / 16); e += 32) {
-            uint4* at = reinterpret_cast<uint4*>(vbuf + v_off<C>(sub * 16 + e / (D / 16), e % (D / 16)));
+          for (int e = lane; e < C::SUB * (D / 16); e += 32) {
+            uint4* at = reinterpret_cast<uint4*>(vbuf + v_off<C>(sub * C::SUB + e / (D / 16), e % (D / 16)));
             const uint4 u = *at;
             uint32_t w[4] = {u.x, u.y, u.z, u.w}, any = 0u;
 #pragma unroll
@@ -568,15 +575,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
             ldsm4t(vf, smem_u32(vbuf + v_off<C>(sub * 16 + (lane & 15), dt * 2 + (lane >> 4))));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              mma16<false>(o[mt][2 * dt], pa[mt], vf[0], vf[1]);
-              mma16<false>(o[mt][2 * dt + 1], pa[mt], vf[2], vf[3]);
+              mma16<false>(o[mt][2 * dt], pa[mt][0], vf[0], vf[1]);
+              mma16<false>(o[mt][2 * dt + 1], pa[mt][0], vf[2], vf[3]);
             }
           }
         } else {
 #pragma unroll
+          for (int ks = 0; ks < C::SUB / 16; ++ks)
+#pragma unroll
           for (int dt = 0; dt < D / 32; ++dt) {
             uint32_t vf[4];
-            ldsm4t(vf, smem_u32(vbuf + v_off<C>(sub * 16 + (lane & 15), dt * 2 + (lane >> 4))));
+            ldsm4t(vf, smem_u32(vbuf + v_off<C>(sub * C::SUB + ks * 16 + (lane & 15), dt * 2 + (lane >> 4))));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               // two keys' codes of an even and an odd dim lie alternately
@@ -585,8 +594,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
               codes_f16(__byte_perm(vf[2 * half + 1], 0u, 0x3120), &e1, &o1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                mma16<true>(o[mt][4 * dt + 2 * half], pa[mt], e0, e1);
-                mma16<true>(o[mt][4 * dt + 2 * half + 1], pa[mt], o0, o1);
+                mma16<true>(o[mt][4 * dt + 2 * half], pa[mt][ks], e0, e1);
+                mma16<true>(o[mt][4 * dt + 2 * half + 1], pa[mt][ks], o0, o1);
               }
             }
           }
