@@ -209,7 +209,7 @@ struct TreeWalk {
 };
 
 // How often the tcgen05 kernel's 128 lanes hold the rows of a block.
-__device__ __forceinline__ int tree_copies(int rows) { return rows <= 32 ? 4 : rows <= 64 ? 2 : 1; }
+__device__ __forceinline__ int tree_copies(int rows) { return rows <= 64 ? 2 : 1; }
 
 // Does query t of element b see drafted node j (both below its count)?
 __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int j) {

@@ -16,11 +16,11 @@
 // S buffers let the QK of tile t+1 run beside the softmax of tile t.  A warp none of
 // whose rows is a query does nothing but keep the barriers going.
 //
-// A block of 64 query rows or fewer has them twice over in the 128 lanes, one of
-// 32 or fewer four times: each copy takes its half or quarter of a key half (its
-// P is zero elsewhere), so the exponentials are spread over all the schedulers
-// instead of staying with the warps of the first rows.  The copies are parts
-// like those of other CTAs, merged with them, or in the CTA for a whole group.
+// A block of 64 query rows or fewer has them twice over in the 128 lanes, and each
+// copy takes half of a key half (its P is zero elsewhere), so the
+// exponentials are spread over all the schedulers instead of staying with the
+// warps of the first rows.  The copies are parts like those of other CTAs, merged
+// with them, or in the CTA for a whole group.
 //
 // bf16 rows: K and V tiles are read by the tensor core where TMA puts them.
 // Masked rows have P = 0, and 0 * NaN would reach every row, so in the tiles
@@ -28,22 +28,24 @@
 // the end, and take a drafted row's NaNs and infinities out of V; the nodes
 // that see such a row get them added at the end.
 //
-// e4m3 rows become bf16 on their way into the same tiles (code * 2^e, exact),
-// so nothing after the tiles knows the difference.  Three warps find the rows of
-// coming tiles and their scales; eight producer warps copy the codes in, convert
-// them and store them.  (Scales
-// applied to logits and probabilities instead, K's codes as an e4m3 operand,
-// took 212 us where this takes 175: the scales cost every logit two operations.
-// Codes brought by TMA and scales by warps of their own took 205.)
+// e4m3 rows become f16 tiles on their way: code * 2^(e - E), E the largest e of the
+// tile's rows (exact down to 2^-15 of it, half of f16's last place off below), so
+// the products run in f16.  2^E of K is a factor of the tile's logits; V's goes into
+// the exponent, p' = 2^(z + E - m'), m' the running maximum of z + E, and the sum
+// takes p' 2^-E.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps
+// find the rows of coming tiles and their scales; eight producer warps copy the
+// codes in, convert them (two instructions for two codes) and store them.
 //
 // Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 92 to
 // 98 us, 5.5 to 5.8 TB/s, 0.84 to 0.89 of the copy rate: HBM, and the
 // exponentials (1024 cycles of a tile's 2600).  4 x 16 nodes over up to 65536
-// e4m3 rows each: 175 us, 0.35 of the floor.  There a tile takes 3300 cycles
-// against the 1300 of its bytes: the conversion is 36 instructions for 16 codes,
-// most of them on a pipe of half rate (900 cycles a scheduler), shared memory 1800,
-// and what is left are each role's chains of latencies, with twenty warps an SM
-// to cover them.  2 x 64 nodes over up to 32768 rows: 111 to 130 us, the same.
+// e4m3 rows each: 161 us, 0.38 of the floor; 2 x 64 nodes over up to 32768 rows: 110.
+// There a tile takes 3200 cycles against the 1300 of its bytes: 1000 of the tensor
+// cores, 1800 of shared memory, and the softmax warps' chain of latencies, which
+// twenty warps on an SM stretch to 2500.  Slower were: bf16 tiles, codes converted by
+// bit moves (175); each row's own scale in the softmax, K's codes as an e4m3 operand
+// (212); codes brought by TMA (205); four or sixteen producers (190, 203); one pass
+// over the logits (185).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -91,8 +93,9 @@ struct TcCfg {
   // kfull, kempty [SK]; vfull, vempty [SV]; s_ready, p_ready, pv_done [2];
   // q_ready, o_free, ml_ready, idle; F8: info_full, info_empty [kInfoRing]
   static constexpr int NBAR = 2 * SK + 2 * SV + 6 + 4 + (F8 ? 2 * kInfoRing : 0);
-  static constexpr int OFF_FLAGS = OFF_BAR + NBAR * 8;  // abort, tmem, odd rows [2][8], ok [kOkRing][4]
-  static constexpr int SMEM = OFF_FLAGS + 8 + 64 + 16 * kOkRing + 1024;  // + alignment
+  // abort, tmem, odd rows [2][8], ok [kOkRing][4], F8: scale bytes [kOkRing][2]
+  static constexpr int OFF_FLAGS = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_FLAGS + 8 + 64 + 16 * kOkRing + (F8 ? 8 * kOkRing : 0) + 1024;  // + alignment
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
@@ -123,6 +126,7 @@ struct TcShared {
   uint32_t* tmem;
   uint32_t* odd;  // [2] by piece: drafted rows with a NaN or an infinity in V, by node
   uint32_t* ok;   // ring of the tiles' rows that were found (paged), 4 words each
+  uint32_t* top;  // F8: ring of the tiles' largest scale bytes of K and of V
 };
 template <class C>
 __device__ __forceinline__ TcShared shared_of(unsigned char* smem) {
@@ -131,6 +135,7 @@ __device__ __forceinline__ TcShared shared_of(unsigned char* smem) {
   s.tmem = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAGS + 4);
   s.odd = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAGS + 8);
   s.ok = s.odd + 16;
+  s.top = s.ok + 4 * kOkRing;
   return s;
 }
 
@@ -204,6 +209,11 @@ __device__ __forceinline__ uint32_t tc_pack(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t tc_pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ void tc_st_x16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -246,7 +256,11 @@ __device__ __forceinline__ f2_t f2_add(f2_t a, f2_t b) {
   return r;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], bf16 operands
+// Both operands bf16, or both f16 (format 0).
+__device__ __forceinline__ constexpr uint32_t tc_idesc(bool f16, int b_mn_major) {
+  return tc::idesc_bf16(128, 128, 0, b_mn_major) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
+}
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -336,43 +350,29 @@ __device__ __forceinline__ void tc_loads(const TreeTcParams& P, unsigned char* s
 }
 
 // ---------------------------------------------------------------- producers (e4m3)
-// Four e4m3 codes as bf16 of value * 2^-120 (sign; exponent and mantissa bits
-// where bf16 has the low ones of its exponent and the high ones of its
-// mantissa): codes 0 and 2, codes 1 and 3.  The columns of K and of V come out
-// with 4w + {1, 2} exchanged, and Q's and O's with them.
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t* h02, uint32_t* h13) {
-  const uint32_t x = w << 8;
-  *h02 = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-  *h13 = (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u);
+// Four e4m3 codes as f16, exactly: codes 0 and 1, codes 2 and 3.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t* h01, uint32_t* h23) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(*h01), "=r"(*h23)
+      : "r"(w));
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-
-// 16 codes at scale byte e as bf16 (two factors: any e).
-__device__ __noinline__ void convert_far(uint4 u, uint32_t e, uint4* lo, uint4* hi) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  const int x = static_cast<int>(e) - 127, x1 = x >> 1;
-  const uint32_t f = e == 255u ? 0x7fff7fffu : (static_cast<uint32_t>(187 + x1) << 7) * 0x10001u;
-  const uint32_t g = e == 255u ? 0x3f803f80u : (static_cast<uint32_t>(187 + x - x1) << 7) * 0x10001u;
-  uint32_t h[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    codes_bf16(w[k], &h[2 * k], &h[2 * k + 1]);
-    h[2 * k] = mul_bf16x2(mul_bf16x2(h[2 * k], g), f);
-    h[2 * k + 1] = mul_bf16x2(mul_bf16x2(h[2 * k + 1], g), f);
-  }
-  *lo = make_uint4(h[0], h[1], h[2], h[3]);
-  *hi = make_uint4(h[4], h[5], h[6], h[7]);
+// 2^(e - top), e <= top, as f16 (zero below its range); NaN for scale byte 255.
+__device__ __forceinline__ uint32_t factor_f16(int e, int top) {
+  const int x = 15 + e - top;  // the biased exponent
+  return e == 255 ? 0x7fffu : x > 0 ? static_cast<uint32_t>(x) << 10 : x > -10 ? 0x200u >> -x : 0u;
 }
 
 // What is known of a row of a tile.
 struct RowInfo {
   long long off;    // of its codes in K and in V; odd: no such row, zeros
-  uint32_t factor;  // 2^(120 + e) as bf16, K's and V's << 16
-  uint32_t bytes;   // scale bytes, K's and V's << 8; bit 31: the tile has an e > 7 (or a NaN), a factor out of range
+  uint32_t factor;  // its scales over the tile's largest, as f16, K's and V's << 16
+  uint32_t unused;
 };
 
 // A finder warp finds the rows of every third tile of the run, lane j rows j + 32 k:
@@ -416,18 +416,22 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
     }
   };
   auto put = [&](int t) {
-    bool far = false;
+    // the tile's largest scales (a NaN row's are left out)
+    uint32_t kt = 0u, vt = 0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (off[k] & 1) kb[k] = vb[k] = 127u;
-      far |= kb[k] > 134u || vb[k] > 134u;
+      if (off[k] & 1) kb[k] = vb[k] = 0u;
+      kt = max(kt, kb[k] == 255u ? 0u : kb[k]);
+      vt = max(vt, vb[k] == 255u ? 0u : vb[k]);
     }
-    const uint32_t flag = __any_sync(0xffffffffu, far) ? 0x80000000u : 0u;
+    kt = __reduce_max_sync(0xffffffffu, kt);
+    vt = __reduce_max_sync(0xffffffffu, vt);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       *reinterpret_cast<uint4*>(&info[(t % kInfoRing) * kRows + 32 * k]) =
           make_uint4(static_cast<uint32_t>(off[k]), static_cast<uint32_t>(off[k] >> 32),
-                     ((kb[k] + 120u) << 7) | ((vb[k] + 120u) << 23), kb[k] | (vb[k] << 8) | flag);
+                     factor_f16(kb[k], kt) | (factor_f16(vb[k], vt) << 16), 0u);
+    if (lane == 0) *reinterpret_cast<uint2*>(sh.top + (t % kOkRing) * 2) = make_uint2(kt, vt);
     tc_arrive_warp(&br.info_full[t % kInfoRing]);
   };
   ask();
@@ -504,38 +508,28 @@ __device__ __forceinline__ void tc_produce(const TreeTcParams& P, unsigned char*
       const unsigned char* src = raw + (h % kRawRing) * (kUnits * 512);
       const RowInfo* rows = info + (t % kInfoRing) * kRows + g * (kRows / kGroups);
       unsigned char* dst = tiles + stage * C::TILEB + g * (kRows / kGroups) * 128;
-      if (__builtin_expect(rows->bytes >> 31, 0)) {
-#pragma unroll 1
-        for (int j = 0; j < kUnits; ++j) {
-          uint4 lo, hi;
-          convert_far(*reinterpret_cast<const uint4*>(src + j * 512), (rows[4 * kSide * j].bytes >> (8 * kv)) & 255u, &lo, &hi);
-          *reinterpret_cast<uint4*>(dst + st0 + j * (kSide * 512)) = lo;
-          *reinterpret_cast<uint4*>(dst + st1 + j * (kSide * 512)) = hi;
-        }
-      } else {
-        // (all loads before the first store: the compiler cannot tell them apart, and
-        // one unit after another ran at 200 cycles a unit)
-        uint4 codes[kUnits];
-        uint32_t factor[kUnits];
+      // (all loads before the first store: the compiler cannot tell them apart, and
+      // one unit after another ran at 200 cycles a unit)
+      uint4 codes[kUnits];
+      uint32_t factor[kUnits];
 #pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-          codes[j] = *reinterpret_cast<const uint4*>(src + j * 512);
-          factor[j] = rows[4 * kSide * j].factor;
-        }
+      for (int j = 0; j < kUnits; ++j) {
+        codes[j] = *reinterpret_cast<const uint4*>(src + j * 512);
+        factor[j] = rows[4 * kSide * j].factor;
+      }
 #pragma unroll
-        for (int j = 0; j < kUnits; ++j) {
-          const uint4 u = codes[j];
-          const uint32_t f = __byte_perm(factor[j], 0, sel);
-          uint32_t x[8];
-          codes_bf16(u.x, &x[0], &x[1]);
-          codes_bf16(u.y, &x[2], &x[3]);
-          codes_bf16(u.z, &x[4], &x[5]);
-          codes_bf16(u.w, &x[6], &x[7]);
+      for (int j = 0; j < kUnits; ++j) {
+        const uint4 u = codes[j];
+        const uint32_t f = __byte_perm(factor[j], 0, sel);
+        uint32_t x[8];
+        codes_f16(u.x, &x[0], &x[1]);
+        codes_f16(u.y, &x[2], &x[3]);
+        codes_f16(u.z, &x[4], &x[5]);
+        codes_f16(u.w, &x[6], &x[7]);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = mul_bf16x2(x[k], f);
-          *reinterpret_cast<uint4*>(dst + st0 + j * (kSide * 512)) = make_uint4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint4*>(dst + st1 + j * (kSide * 512)) = make_uint4(x[4], x[5], x[6], x[7]);
-        }
+        for (int k = 0; k < 8; ++k) x[k] = mul_f16x2(x[k], f);
+        *reinterpret_cast<uint4*>(dst + st0 + j * (kSide * 512)) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(dst + st1 + j * (kSide * 512)) = make_uint4(x[4], x[5], x[6], x[7]);
       }
       if (g == kGroups - 1) {
         tc::fence_async_smem();
@@ -603,7 +597,7 @@ __device__ __forceinline__ void tc_mma(const TreeTcParams& P, unsigned char* sme
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-        tc::mma_bf16_ss(tmem + b * 128, qd + off, ks + off, tc::idesc_bf16(128, 128, 0, 0), kk > 0 ? 1u : 0u);
+        tc::mma_bf16_ss(tmem + b * 128, qd + off, ks + off, tc_idesc(C::F8, 0), kk > 0 ? 1u : 0u);
       }
       tc::commit(&br.kempty[stage]);
       tc::commit(&br.s_ready[b]);
@@ -631,7 +625,7 @@ __device__ __forceinline__ void tc_mma(const TreeTcParams& P, unsigned char* sme
         for (int kt = 0; kt < 8; ++kt) {
           // keys 0-63 into O_a (column 256), 64-127 into O_b (384); P's half at its S half
           const uint32_t a = tmem + b * 128 + (kt >> 2) * 64 + (kt & 3) * 8;
-          mma_ts(tmem + 256 + (kt >> 2) * 128, a, vst + kt * 128, tc::idesc_bf16(128, 128, 0, 1),
+          mma_ts(tmem + 256 + (kt >> 2) * 128, a, vst + kt * 128, tc_idesc(C::F8, 1),
                  ((kt & 3) > 0 || u > 0) ? 1u : 0u);
         }
         tc::commit(&br.vempty[vs]);
@@ -679,6 +673,7 @@ __device__ __noinline__ unsigned long long seen_bits(const TreeParams& p, const 
 
 // Half h of row r of a V tile: zeros where the row is gone; in drafted rows
 // (node >= 0) NaNs and infinities become zeros, and the node is marked.
+template <bool F8>
 __device__ __noinline__ void clean_row(unsigned char* v, int r, int h, bool gone, int node, uint32_t* odd_rows) {
   if (!gone && node < 0) return;
   bool odd = false;
@@ -690,7 +685,8 @@ __device__ __noinline__ void clean_row(unsigned char* v, int r, int h, bool gone
     bool here = gone;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const bool lo = (w[k] & 0x7f80u) == 0x7f80u, hi = (w[k] & 0x7f800000u) == 0x7f800000u;
+      constexpr uint32_t kExp = F8 ? 0x7c00u : 0x7f80u;  // of f16, bf16
+      const bool lo = (w[k] & kExp) == kExp, hi = (w[k] & (kExp << 16)) == kExp << 16;
       here |= lo | hi;
       if (gone || lo) w[k] &= 0xffff0000u;
       if (gone || hi) w[k] &= 0xffffu;
@@ -699,15 +695,6 @@ __device__ __noinline__ void clean_row(unsigned char* v, int r, int h, bool gone
     odd |= here;
   }
   if (odd && !gone) atomicOr(&odd_rows[node >> 5], 1u << (node & 31));
-}
-
-// A finite code at scale byte e as the producers' bf16, infinite above its range.
-__device__ __forceinline__ float odd_e4m3(uint32_t code, int e) {
-  uint32_t a, b;
-  codes_bf16(code, &a, &b);
-  const int x = e - 127, x1 = x >> 1;
-  a = mul_bf16x2(a, static_cast<uint32_t>(127 + 60 + x - x1) << 7);
-  return __uint_as_float(mul_bf16x2(a, static_cast<uint32_t>(127 + 60 + x1) << 7) << 16);
 }
 
 // Adds the NaNs and infinities of the marked drafted rows that `node` sees to its
@@ -724,9 +711,9 @@ __device__ __noinline__ void add_odd(const TreeParams& p, const TreePiece& pc, i
 #pragma unroll 1
     for (int j = 0; j < 64; ++j) {
       float y;
-      if (F8) {  // a NaN row, or a code whose value is above bf16's range
-        const int e = p.cache.vs[at.sc + pc.g * p.cache.ss_head];
-        y = e == 255 ? __uint_as_float(0x7fffffffu) : odd_e4m3(p.cache.v[v + j], e);
+      if (F8) {  // a NaN row (or a code that no writer makes)
+        const bool nan = p.cache.vs[at.sc + pc.g * p.cache.ss_head] == 255 || (p.cache.v[v + j] & 0x7f) == 0x7f;
+        y = nan ? __uint_as_float(0x7fffffffu) : 0.f;
       } else {
         y = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p.cache.v)[v + j]) << 16);
       }
@@ -775,8 +762,7 @@ __device__ __noinline__ bool merge_copies(const CopyMerge& m, uint32_t phase) {
     float o[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      const int to = C::F8 ? (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1) : j;  // the producers' order
-      o[to] = fmaf(__uint_as_float(a[j >> 4][j & 15]), m.fa, __uint_as_float(b[j >> 4][j & 15]) * m.fb);
+      o[j] = fmaf(__uint_as_float(a[j >> 4][j & 15]), m.fa, __uint_as_float(b[j >> 4][j & 15]) * m.fb);
     }
     unsigned char* mine = m.qbuf + m.li * 256 + m.hf * 128;
     if (m.copy > 0)
@@ -850,16 +836,41 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
     const bool warp_live = (pc.mb * kRows + (quarter * 32) % span) / p.G < pc.e.cnt;
     const int k0 = copy * (64 / copies);  // the copy's keys of the half: k0 .. k0 + 64 / copies - 1
     const int first_draft = pc.e.n - pc.e.cnt;
+    float row_log2 = p.scale_log2;  // F8: with the row's power of two
     if (warp_live) {
       const unsigned char* src = p.q + 2 * (pc.b * p.q_batch + node * p.q_token + head * p.q_head);
+      float f1 = 1.f, f2 = 1.f;
+      if (C::F8) {
+        // as f16, scaled by a power of two to below 2 (exact for elements down to 2^-14
+        // of the row's largest, half of 2^-24 off below)
+        uint32_t mx = 0u;
+        if (live)
+#pragma unroll 4
+          for (int ch = 0; ch < 16; ++ch) {
+            const uint4 v = *reinterpret_cast<const uint4*>(src + ch * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+          }
+        int ex = static_cast<int>(mx >> 7);  // biased exponent of the row's largest element
+        if (ex == 0 || ex == 255) ex = 127;
+        // it comes off in two factors: 2^-(ex - 127) may be out of fp32's range
+        const int e1 = (ex - 127) / 2, e2 = ex - 127 - e1;
+        f1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+        f2 = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+        row_log2 *= __uint_as_float(static_cast<uint32_t>(ex) << 23);
+      }
 #pragma unroll
       for (int c8 = 0; c8 < 8; ++c8) {
         const int ch = hf * 8 + c8;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (live) v = *reinterpret_cast<const uint4*>(src + ch * 16);
-        if (C::F8)  // the producers' order of the columns
-          v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
-                         __byte_perm(v.z, v.w, 0x7632));
+        if (C::F8) {
+          v.x = tc_pack_f16(bf16lo(v.x) * f1 * f2, bf16hi(v.x) * f1 * f2);
+          v.y = tc_pack_f16(bf16lo(v.y) * f1 * f2, bf16hi(v.y) * f1 * f2);
+          v.z = tc_pack_f16(bf16lo(v.z) * f1 * f2, bf16hi(v.z) * f1 * f2);
+          v.w = tc_pack_f16(bf16lo(v.w) * f1 * f2, bf16hi(v.w) * f1 * f2);
+        }
         *reinterpret_cast<uint4*>(qbuf + tile_off(i, ch)) = v;
       }
       tc::fence_async_smem();
@@ -874,6 +885,8 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       if (!tc_wait_warp(&br.s_ready[b], (t >> 1) & 1, sh.abort, p.status)) return;
       const int tile_row = u * kRows;
       const int kb = tile_row + hf * 64;
+      uint2 top = make_uint2(127u, 127u);
+      if (C::F8) top = *reinterpret_cast<const uint2*>(sh.top + (t % kOkRing) * 2);
       bool found_all = true;
       const volatile uint32_t* okw = sh.ok + (t % kOkRing) * 4;
       if (p.cache.bt)  // written before the tile's rows were asked for; ten tiles on, this one's PV is done
@@ -885,28 +898,37 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         if (!found_all) there = okw[2 * hf] | (static_cast<unsigned long long>(okw[2 * hf + 1]) << 32);
         vis = live ? seen_bits(p, pc, node, kb) & there : 0ull;
       }
+      // F8: the tile's K scale is the logit's, its V scale is taken into the exponent
+      // (p' = 2^(z + e - m'), and the sum takes p' 2^-e), f16's range from the top
+      float per_s = p.scale_log2, v_exp = 0.f, v_inv = 1.f;
+      if (C::F8) {
+        per_s = fminf(fmaxf(row_log2 * __uint_as_float(max(top.x, 1u) << 23), 1.17549435e-38f), 3.4e38f);
+        v_exp = static_cast<float>(static_cast<int>(top.y) - 127);
+        v_inv = __uint_as_float(max(254 - static_cast<int>(top.y), 1) << 23);
+      }
       if (warp_live) {
         // both passes read the logits from tensor memory, 32 columns a turn: the
         // loops stay small (all 64 in registers made the kernel's loops together
         // larger than the SM's instruction cache); a quarter's 16 stay in registers
         const uint32_t ts = tl + b * 128 + hf * 64;
         float mraw = NEG;
-        uint32_t few[1][16];
-        if (copies == 4) {
+        uint32_t few[2][16];
+        if (copies == 2) {
           tc::ld_32x32b_x16(ts + k0, few[0]);
-          tc_wait_ld<1>(few);
+          tc::ld_32x32b_x16(ts + k0 + 16, few[1]);
+          tc_wait_ld<2>(few);
           if (__builtin_expect(special, 0)) {
             const uint32_t v = static_cast<uint32_t>(vis >> k0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (!((v >> j) & 1u)) few[0][j] = __float_as_uint(NEG);
+            for (int j = 0; j < 32; ++j)
+              if (!((v >> j) & 1u)) few[j >> 4][j & 15] = __float_as_uint(NEG);
           }
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            mraw = fmaxf(mraw, fmaxf(__uint_as_float(few[0][j]), __uint_as_float(few[0][j + 1])));
+          for (int j = 0; j < 32; j += 2)
+            mraw = fmaxf(mraw, fmaxf(__uint_as_float(few[j >> 4][j & 15]), __uint_as_float(few[j >> 4][(j + 1) & 15])));
         } else {
 #pragma unroll 1
-          for (int c = k0; c < k0 + 64 / copies; c += 32) {
+          for (int c = 0; c < 64; c += 32) {
             uint32_t r[2][16];
             tc::ld_32x32b_x16(ts + c, r[0]);
             tc::ld_32x32b_x16(ts + c + 16, r[1]);
@@ -925,7 +947,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
               mraw = fmaxf(mraw, fmaxf(__uint_as_float(r[j >> 4][j & 15]), __uint_as_float(r[j >> 4][(j + 1) & 15])));
           }
         }
-        const float mx = mraw * p.scale_log2;
+        const float mx = fmaf(mraw, per_s, v_exp);
         const bool grow = mx > m_used + 8.f;
         const bool rescale = grow && m_used != NEG;
         if (__any_sync(FULL, rescale)) {
@@ -944,8 +966,8 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           lsum *= f;
         }
         if (grow) m_used = mx;
-        const float neg = m_used == NEG ? 0.f : -m_used;
-        const f2_t neg2 = f2(neg, neg), sl2 = f2(p.scale_log2, p.scale_log2);
+        const float neg = (m_used == NEG ? 0.f : -m_used) + (C::F8 ? v_exp + 6.f : 0.f);
+        const f2_t neg2 = f2(neg, neg), sl2 = f2(per_s, per_s);
         f2_t sum2 = f2(0.f, 0.f);
         auto prob = [&](const uint32_t* x) -> uint32_t {  // two columns' probabilities, packed
           float p0, p1;
@@ -953,23 +975,20 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           p0 = tc_ex2(p0);
           p1 = tc_ex2(p1);
           sum2 = f2_add(f2(p0, p1), sum2);
-          return tc_pack(p0, p1);
+          return C::F8 ? tc_pack_f16(p0, p1) : tc_pack(p0, p1);
         };
         // P's columns (two keys each) take the place of logits that were read
-        if (copies == 4) {
-          uint32_t w[2][16];
+        uint32_t w[16];
+        if (copies == 2) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t x = prob(&few[0][2 * e]);
+          for (int e = 0; e < 16; ++e) w[e] = prob(&few[e >> 3][(2 * e) & 15]);
+          tc_st_x16(ts + k0 / 2, w);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) w[q >> 1][(q & 1) * 8 + e] = copy == q ? x : 0u;
-          }
-          tc_st_x16(ts, w[0]);
-          tc_st_x16(ts + 16, w[1]);
+          for (int e = 0; e < 16; ++e) w[e] = 0u;
+          tc_st_x16(ts + 16 * (1 - copy), w);
         } else {
-          uint32_t w[16];
 #pragma unroll 1
-          for (int c = k0; c < k0 + 64 / copies; c += 32) {
+          for (int c = 0; c < 64; c += 32) {
             uint32_t r[2][16];
             tc::ld_32x32b_x16(ts + c, r[0]);
             tc::ld_32x32b_x16(ts + c + 16, r[1]);
@@ -978,16 +997,11 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
             for (int e = 0; e < 16; ++e) w[e] = prob(&r[e >> 3][(2 * e) & 15]);
             tc_st_x16(ts + c / 2, w);
           }
-          if (copies == 2) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = 0u;
-            tc_st_x16(ts + 16 * (1 - copy), w);
-          }
         }
         {
           float s0, s1;
           f2_split(sum2, &s0, &s1);
-          lsum += s0 + s1;
+          lsum = fmaf(s0 + s1, v_inv, lsum);
         }
         tc_wait_st();
       }
@@ -997,7 +1011,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         if (!tc_wait_warp(&br.vfull[stage], (t / C::SV) & 1, sh.abort, p.status)) return;
         const int r = threadIdx.x >> 1;  // two threads a row
         const bool gone = tile_row + r >= pc.e.n || (!found_all && !((okw[r >> 5] >> (r & 31)) & 1u));
-        clean_row(smem + C::OFF_V + stage * C::TILEB, r, threadIdx.x & 1, gone, tile_row + r - first_draft, odd_rows);
+        clean_row<C::F8>(smem + C::OFF_V + stage * C::TILEB, r, threadIdx.x & 1, gone, tile_row + r - first_draft, odd_rows);
         tc::fence_async_smem();
       }
       tc::fence_before_sync();
@@ -1040,8 +1054,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         float o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int col = C::F8 ? (j & ~3) | ((j & 1) << 1) | ((j >> 1) & 1) : j;  // the producers' order
-          o[col] = fmaf(__uint_as_float(ab[0][j]), fa, __uint_as_float(ab[1][j]) * fb) * unit;
+          o[j] = fmaf(__uint_as_float(ab[0][j]), fa, __uint_as_float(ab[1][j]) * fb) * unit;
         }
         if (live) {
           if (whole) {

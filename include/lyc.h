@@ -555,10 +555,11 @@ lyc_status lyc_cache_read(const lyc_layer_cache* cache, const lyc_read_args* arg
  * lies in rows not seen, NaN included, does not reach the output.  Queries
  * t >= t_len[b] are padding: not read, outputs as they were.  1 <= T <= 256.
  * Scores, sums and the softmax are fp32; the probabilities are rounded to the
- * 16-bit type of the second product: bf16, or over an E4M3 cache with up to 32
- * query rows a KV head, fp16 together with the row's V scale.  There what is
- * below 2^-30 of a query's largest probability * scale is lost, and a query's
- * elements below 2^-17 of its largest are rounded to 2^-24 of that.  The result of a call does not depend on
+ * 16-bit type of the second product: bf16, or over an E4M3 cache fp16 together
+ * with V's scale.  There what is below 2^-30 of a query's largest probability *
+ * scale is lost, and a query's elements below 2^-17 of its largest are rounded
+ * to 2^-24 of that; with more than 32 query rows a KV head, so are K's and V's
+ * elements below 2^-15 of the largest scale of their 128 rows.  The result of a call does not depend on
  * the order in which the GPU runs its blocks.
  *   q, out  [batch][T][num_q_heads][head_dim] bf16, num_q_heads a multiple of
  *           num_kv_heads

@@ -86,10 +86,9 @@ def sees(mask, b, t, j):
 def tree(q, cache, n, t_len, mask, scale):
     """(out, bound) [B][T][Hq][d] float64; NaN where a query is padding.
 
-    Bound: each probability carries its rounding u and e^delta - 1.  u is bf16's:
-    bf16 rows, and e4m3 rows on the tcgen05 kernel, whose tiles are bf16, take
-    probabilities p(1 + r), |r| <= 2^-8 (8 significant bits, to nearest); the
-    mma.sync kernel's fp16 over e4m3 rows is within that (2^-11).  delta is what fp32
+    Bound: each probability carries its rounding u and e^delta - 1.  u is bf16's
+    for both caches: p(1 + r), |r| <= 2^-8 (8 significant bits, to nearest); the fp16
+    of e4m3 rows is within that (2^-11).  delta is what fp32
     does to a logit: d + 8 roundoffs of sum |q k| scale, and four of the logit in
     log2 units (at most 1.5 times it, plus 130 for a scale's exponent); over an e4m3
     cache also what a query's elements lose as fp16 under the row's largest, scaled
