@@ -206,7 +206,9 @@ struct TmLoader {
         s[r] = kb[k] == 255 ? nan : __uint_as_float(static_cast<uint32_t>(kb[k]) << 23);
         s[C::KC + r] = vb[k] == 255 ? nan : static_cast<float>(vb[k] - 127);
         // finite for a NaN row too: its exponent makes p NaN where it is seen, and 0 * NaN is not 0 where not
-        s[2 * C::KC + r] = vb[k] == 255 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(254 - vb[k], 1)) << 23);
+        s[2 * C::KC + r] = vb[k] == 255   ? 1.f
+                           : vb[k] == 254 ? __uint_as_float(0x00400000u)
+                                          : __uint_as_float(static_cast<uint32_t>(254 - vb[k]) << 23);
       }
     }
     pending = -1;

@@ -29,23 +29,27 @@
 // that see such a row get them added at the end.
 //
 // e4m3 rows become f16 tiles on their way: code * 2^(e - E), E the largest e of the
-// tile's rows (exact down to 2^-15 of it, half of f16's last place off below), so
-// the products run in f16.  2^E of K is a factor of the tile's logits; V's goes into
-// the exponent, p' = 2^(z + E - m'), m' the running maximum of z + E, and the sum
-// takes p' 2^-E.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps
-// find the rows of coming tiles and their scales; eight producer warps copy the
-// codes in, convert them (two instructions for two codes) and store them.
+// tile's rows, so the products run in f16.  2^E of K is a factor of the tile's
+// logits; V's goes into the exponent, p' = 2^(z + E - m'), m' the running maximum of
+// z + E, and the sum
+// takes p' 2^-E.  That is exact while the tile's e are within 15 of each other; where
+// they are not (a row of zeros; a drafted row that nobody has written or sees), the
+// tile is the codes alone and the softmax warps apply each row's scales.  A query
+// row becomes f16 as in tree_mma_kernel.cu.  Three warps find the rows of coming
+// tiles and their scales; eight producer warps copy the codes in, convert them
+// (two instructions for two codes) and store them.
 //
 // Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 92 to
 // 98 us, 5.5 to 5.8 TB/s, 0.84 to 0.89 of the copy rate: HBM, and the
 // exponentials (1024 cycles of a tile's 2600).  4 x 16 nodes over up to 65536
-// e4m3 rows each: 161 us, 0.38 of the floor; 2 x 64 nodes over up to 32768 rows: 110.
+// e4m3 rows each: 166 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 117.
 // There a tile takes 3200 cycles against the 1300 of its bytes: 1000 of the tensor
 // cores, 1800 of shared memory, and the softmax warps' chain of latencies, which
 // twenty warps on an SM stretch to 2500.  Slower were: bf16 tiles, codes converted by
 // bit moves (175); each row's own scale in the softmax, K's codes as an e4m3 operand
-// (212); codes brought by TMA (205); four or sixteen producers (190, 203); one pass
-// over the logits (185).
+// (212); codes brought by TMA (205); four or sixteen producers (190, 203); a fourth
+// finder (200: the schedulers' warps are no longer the same); one pass over the
+// logits (185).  Leaving out the check of the scales' spread gained 4.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -121,12 +125,14 @@ struct TcBars {
   }
 };
 
+constexpr uint32_t kOwn = 0x100u;
+
 struct TcShared {
   int* abort;
   uint32_t* tmem;
   uint32_t* odd;  // [2] by piece: drafted rows with a NaN or an infinity in V, by node
   uint32_t* ok;   // ring of the tiles' rows that were found (paged), 4 words each
-  uint32_t* top;  // F8: ring of the tiles' largest scale bytes of K and of V
+  uint32_t* top;  // F8: ring of the tiles' largest scale bytes of K (kOwn: rows have their own) and of V
 };
 template <class C>
 __device__ __forceinline__ TcShared shared_of(unsigned char* smem) {
@@ -362,7 +368,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 2^(e - top), e <= top, as f16 (zero below its range); NaN for scale byte 255.
+// 2^(e - top), e <= top, as f16; NaN for scale byte 255.  (A row that is not there has any factor.)
 __device__ __forceinline__ uint32_t factor_f16(int e, int top) {
   const int x = 15 + e - top;  // the biased exponent
   return e == 255 ? 0x7fffu : x > 0 ? static_cast<uint32_t>(x) << 10 : x > -10 ? 0x200u >> -x : 0u;
@@ -372,7 +378,7 @@ __device__ __forceinline__ uint32_t factor_f16(int e, int top) {
 struct RowInfo {
   long long off;    // of its codes in K and in V; odd: no such row, zeros
   uint32_t factor;  // its scales over the tile's largest, as f16, K's and V's << 16
-  uint32_t unused;
+  uint32_t own;     // its scale bytes, V's << 8
 };
 
 // A finder warp finds the rows of every third tile of the run, lane j rows j + 32 k:
@@ -416,22 +422,35 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
     }
   };
   auto put = [&](int t) {
-    // the tile's largest scales (a NaN row's are left out)
-    uint32_t kt = 0u, vt = 0u;
+    // the tile's largest scales and 255 less its smallest (a NaN row's are left out)
+    uint32_t kt = 0u, vt = 0u, kl = 0u, vl = 0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (off[k] & 1) kb[k] = vb[k] = 0u;
-      kt = max(kt, kb[k] == 255u ? 0u : kb[k]);
-      vt = max(vt, vb[k] == 255u ? 0u : vb[k]);
+      const bool have = (off[k] & 1) == 0;
+      if (have && kb[k] != 255u) {
+        kt = max(kt, kb[k]);
+        kl = max(kl, 255u - kb[k]);
+      }
+      if (have && vb[k] != 255u) {
+        vt = max(vt, vb[k]);
+        vl = max(vl, 255u - vb[k]);
+      }
     }
     kt = __reduce_max_sync(0xffffffffu, kt);
     vt = __reduce_max_sync(0xffffffffu, vt);
+    kl = __reduce_max_sync(0xffffffffu, kl);
+    vl = __reduce_max_sync(0xffffffffu, vl);
+    // codes are multiples of 2^-9, f16's last place is 2^-24
+    const bool own = kt + kl > 255u + 15u || vt + vl > 255u + 15u;
+    if (own) kt = vt = 127u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+      const int ke = own && kb[k] != 255u ? 127 : kb[k], ve = own && vb[k] != 255u ? 127 : vb[k];
       *reinterpret_cast<uint4*>(&info[(t % kInfoRing) * kRows + 32 * k]) =
           make_uint4(static_cast<uint32_t>(off[k]), static_cast<uint32_t>(off[k] >> 32),
-                     factor_f16(kb[k], kt) | (factor_f16(vb[k], vt) << 16), 0u);
-    if (lane == 0) *reinterpret_cast<uint2*>(sh.top + (t % kOkRing) * 2) = make_uint2(kt, vt);
+                     factor_f16(ke, kt) | (factor_f16(ve, vt) << 16), kb[k] | (vb[k] << 8));
+    }
+    if (lane == 0) *reinterpret_cast<uint2*>(sh.top + (t % kOkRing) * 2) = make_uint2(kt | (own ? kOwn : 0u), vt);
     tc_arrive_warp(&br.info_full[t % kInfoRing]);
   };
   ask();
@@ -630,6 +649,7 @@ __device__ __forceinline__ void tc_mma(const TreeTcParams& P, unsigned char* sme
         }
         tc::commit(&br.vempty[vs]);
         tc::commit(&br.pv_done[b]);
+        if (C::F8) tc::commit(&br.info_empty[t % kInfoRing]);  // the softmax is done with the tile's rows, too
       }
       __syncwarp();
       ++t;
@@ -805,6 +825,44 @@ __device__ __noinline__ bool merge_copies(const CopyMerge& m, uint32_t phase) {
 }
 constexpr uint32_t kMergeWaits = 5;
 
+// A tile whose rows have their own scales: n columns of logits from `col` on become
+// z + e in log2 units (e of V), -inf where `vis` is not set.
+__device__ __noinline__ void own_logits(uint32_t col, int n, const RowInfo* own, float per_s, unsigned long long vis) {
+#pragma unroll 1
+  for (int c = 0; c < n; c += 16) {
+    uint32_t r[1][16];
+    tc::ld_32x32b_x16(col + c, r[0]);
+    tc_wait_ld<1>(r);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t k = own[c + j].own & 255u, v = own[c + j].own >> 8;
+      const float kf = k == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(max(k, 1u) << 23);
+      const float ev = v == 255u ? 0.f : static_cast<float>(static_cast<int>(v) - 127);  // (its V row is NaN itself)
+      const float x = fmaf(__uint_as_float(r[0][j]) * per_s, kf, ev);
+      r[0][j] = (vis >> (c + j)) & 1ull ? __float_as_uint(x) : __float_as_uint(-INFINITY);
+    }
+    tc_st_x16(col + c, r[0]);
+  }
+  tc_wait_st();
+}
+// ... and the sum of 2^(z + neg) over them.
+__device__ __noinline__ float own_sum(uint32_t col, int n, const RowInfo* own, float neg) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < n; c += 16) {
+    uint32_t r[1][16];
+    tc::ld_32x32b_x16(col + c, r[0]);
+    tc_wait_ld<1>(r);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint32_t v = own[c + j].own >> 8;
+      const float ev = v == 255u ? 0.f : static_cast<float>(static_cast<int>(v) - 127);
+      sum += tc_ex2(__uint_as_float(r[0][j]) - ev + neg);
+    }
+  }
+  return sum;
+}
+
 template <class C>
 __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char* smem, uint32_t tmem) {
   const TreeParams& p = P.t;
@@ -902,15 +960,22 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       // (p' = 2^(z + e - m'), and the sum takes p' 2^-e), f16's range from the top
       float per_s = p.scale_log2, v_exp = 0.f, v_inv = 1.f;
       if (C::F8) {
-        per_s = fminf(fmaxf(row_log2 * __uint_as_float(max(top.x, 1u) << 23), 1.17549435e-38f), 3.4e38f);
+        per_s = fminf(fmaxf(row_log2 * __uint_as_float(max(top.x & 255u, 1u) << 23), 1.17549435e-38f), 3.4e38f);
         v_exp = static_cast<float>(static_cast<int>(top.y) - 127);
-        v_inv = __uint_as_float(max(254 - static_cast<int>(top.y), 1) << 23);
+        v_inv = __uint_as_float(top.y == 254u ? 0x00400000u : (254u - top.y) << 23);
       }
       if (warp_live) {
         // both passes read the logits from tensor memory, 32 columns a turn: the
         // loops stay small (all 64 in registers made the kernel's loops together
         // larger than the SM's instruction cache); a quarter's 16 stay in registers
         const uint32_t ts = tl + b * 128 + hf * 64;
+        const bool own = C::F8 && (top.x & kOwn) != 0u;
+        const RowInfo* own_row = reinterpret_cast<const RowInfo*>(smem + C::OFF_INFO) + (t % kInfoRing) * kRows + hf * 64 + k0;
+        if (__builtin_expect(own, 0)) {
+          own_logits(ts + k0, 64 / copies, own_row, row_log2, vis >> k0);
+          per_s = 1.f;
+          v_inv = 0.f;  // the sum is own_sum's
+        }
         float mraw = NEG;
         uint32_t few[2][16];
         if (copies == 2) {
@@ -967,6 +1032,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         }
         if (grow) m_used = mx;
         const float neg = (m_used == NEG ? 0.f : -m_used) + (C::F8 ? v_exp + 6.f : 0.f);
+        if (__builtin_expect(own, 0)) lsum += own_sum(ts + k0, 64 / copies, own_row, neg);
         const f2_t neg2 = f2(neg, neg), sl2 = f2(per_s, per_s);
         f2_t sum2 = f2(0.f, 0.f);
         auto prob = [&](const uint32_t* x) -> uint32_t {  // two columns' probabilities, packed
@@ -1109,7 +1175,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_tc_kernel(const __grid_con
     if (C::F8)
       for (int s = 0; s < kInfoRing; ++s) {
         mbar_init(&br.info_full[s], 1);
-        mbar_init(&br.info_empty[s], kProducers);
+        mbar_init(&br.info_empty[s], kProducers + 1);
       }
     *sh.abort = 0;
     fence_mbar_init();

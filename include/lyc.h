@@ -558,8 +558,8 @@ lyc_status lyc_cache_read(const lyc_layer_cache* cache, const lyc_read_args* arg
  * 16-bit type of the second product: bf16, or over an E4M3 cache fp16 together
  * with V's scale.  There what is below 2^-30 of a query's largest probability *
  * scale is lost, and a query's elements below 2^-17 of its largest are rounded
- * to 2^-24 of that; with more than 32 query rows a KV head, so are K's and V's
- * elements below 2^-15 of the largest scale of their 128 rows.  The result of a call does not depend on
+ * to 2^-24 of that.  (There the scales of rows that are not seen may choose
+ * between two roundings.)  The result of a call does not depend on
  * the order in which the GPU runs its blocks.
  *   q, out  [batch][T][num_q_heads][head_dim] bf16, num_q_heads a multiple of
  *           num_kv_heads

@@ -614,6 +614,48 @@ def test_tree_scales_of_every_size(lyc, T, page):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,hq,page", [(6, 2, 0), (12, 4, 16), (40, 4, 0), (130, 1, 16)])
+def test_tree_rows_that_nobody_wrote(lyc, e4m3, T, hq, page):
+    """Drafted rows that no node sees hold any bytes at all (codes and scales of every
+    value, or bf16 bits): the outputs are those over rows of zeros, to the bit, except
+    that with many query rows over an e4m3 cache the scales of a tile's rows choose
+    between two ways to scale its products, each within the bound."""
+    n, cap = [T + 333, T, T + 120], T + 352 - T % 16
+    rng = np.random.default_rng(T)
+    mask = random_tree(rng, 3, T)
+    dead = [t for t in range(T) if t % 3 == 1]
+    words = mask.cpu().numpy().view(np.uint64)
+    for t in dead:
+        words[:, :, t // 64] &= np.uint64(2**64 - 1 - (1 << (t % 64)))
+    mask = torch.from_numpy(words.view(np.int64)).cuda()
+    cache = fill(lyc, 3, 1, 128, cap, page, e4m3, seed=T)
+    poison_past(cache, n)
+    k, v, ks, vs, bt = cache.tensors
+    q = randn(9, 3, T, hq, 128)
+    for kind in range(4):  # zeros, any bytes, the largest scales and codes, NaN codes
+        for x in (k, v, ks, vs):
+            if x is None:
+                continue
+            b8 = x.view(torch.uint8)
+            for b in range(3):
+                for t in dead:
+                    row = n[b] - T + t
+                    at = (b, 0, row) if bt is None else (int(bt[b, row // page]), row % page, 0)
+                    if kind == 1:
+                        b8[at] = torch.randint(0, 256, b8[at].shape, device="cuda", dtype=torch.uint8)
+                    else:
+                        b8[at] = (0, 0, 254, 127)[kind]
+        if kind == 0:
+            zeros = check_tree(lyc, cache, q, n, None, mask, what="zeros")
+            want, bound = SO.tree(q, cache, n, [T] * 3, mask, 128**-0.5)
+        out, st = run_tree(lyc, cache, q, n, None, mask)
+        assert st == 0
+        SO.close(out, want, bound, f"kind {kind}")
+        if not (e4m3 and T * hq > 32):
+            assert torch.equal(out, zeros), kind
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("T", [4, 20])
 def test_tree_cache_orders(lyc, e4m3, T):
     """The same rows in other orders and with padding between them: rows before
