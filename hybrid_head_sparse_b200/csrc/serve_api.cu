@@ -149,14 +149,16 @@ int sm_count(int device) {
   return sms;
 }
 
-// The tcgen05 kernel has query blocks of 128 rows, the mma.sync kernel of 16 or 32.
-// Its blocks read the cache again, so above 32 rows it loses: 36 rows over 131072
-// cached rows (32/8 heads, us) mma.sync 193 bf16 and 262 e4m3, tcgen05 92 and 116;
-// over 2048 rows 16.0 and 16.0 to 15.8 and 20.5.  Within 32 rows the longest caches
-// would gain and the others lose (32 rows over 131072: 99 and 134 to 97 and 120;
-// over 2048: 14 and 15 to 20 and 25; 16 elements of 1024: 35 and 32 to 36 and 44),
-// and a capacity says little of the lengths.
-constexpr int kMmaMostRows = 32;
+// The most query rows of a KV head that the mma.sync kernel takes where the tcgen05
+// kernel could.  Times in us, 32/8 heads of 128, over 131072 rows, 4 x 8192, 2048, 16 x
+// 1024 and 32 x 300:
+//   bf16, 16 rows   mma.sync  87   33  10.5  23  25
+//   bf16, 32 rows   mma.sync  99   43  14    35  42   tcgen05  90  35  15  30  43
+//   e4m3, 32 rows   mma.sync 121   42  15    32  37   tcgen05 106  49  20  42  60
+//   e4m3, 36 rows   mma.sync 214   62  16    51  57   tcgen05 108  50  22  44  62
+// (mma.sync has blocks of 16 or 32 rows, so more read the cache again; the capacity
+// that the host knows says little of the lengths.)
+constexpr int mma_most_rows(int cache_type) { return cache_type == LYC_CACHE_BF16 ? 16 : 32; }
 
 struct TreeShape {
   bool tc;  // the tcgen05 kernel
@@ -178,7 +180,7 @@ bool tree_shape(const lyc_layer_cache* c, int T, int Hq, bool may_tc, TreeShape*
   const int sms = sm_count(c->device);
   if (sms < 1) return false;
   const int rows = Hq / c->num_kv_heads * T;
-  s->tc = may_tc && c->head_dim == 128 && rows > kMmaMostRows &&
+  s->tc = may_tc && c->head_dim == 128 && rows > mma_most_rows(c->type) &&
           (c->type == LYC_CACHE_E4M3 || tree_tc_box_rows(view(c)) > 0);
   s->block_rows = s->tc ? 128 : tree_mma_block_rows(rows);
   s->tile_rows = s->tc ? 128 : tree_mma_tile_rows(c->head_dim, c->type);
