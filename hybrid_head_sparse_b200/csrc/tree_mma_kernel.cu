@@ -279,13 +279,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
       tree_elem(p, b, &bad);
       if (bad) atomicOr(p.status, LYC_OP_BAD_LENGTH);
     }
-  const TreeSched<C::TR, C::ROWS> sched(p);
+  TreeSched<C::TR, C::ROWS> sched(p);
   const int cta = blockIdx.x;
   const float NEG = -INFINITY;
   const uint32_t xend = sched.begin(cta + 1);
 
   for (uint32_t x = sched.begin(cta); x < xend;) {
-    const TreePiece pc = piece_at(sched, x, xend);
+    const TreePiece pc = piece_at<C::TR, C::ROWS>(sched, x, xend);
     x += pc.t1 - pc.t0;
     const int first_draft = pc.e.n - pc.e.cnt;
     TmLoader<C> ld(p, pc, smem, warp, lane);
@@ -672,31 +672,57 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
   }
 }
 
-// One warp for each query row of each group: merges the states of the CTAs
-// among which the group was cut, in their order.  The lengths are inputs of
-// the whole call, complete before the attention kernel lets this one start,
-// so the division of work is computed while that one runs; then the rows of
+// A warp for a query row (4 y + warp of its block of rows) of each group that may have
+// been cut: merges the states of the CTAs among which it was, in their order.
+// Blocks x are the groups, or where those are more than the CTAs (of which each cuts
+// one at most; a warp for each row of 1024 elements' groups took as long as the
+// attention) the CTAs: the group in which the next CTA's run starts, unless an
+// earlier run starts in it, too.  The lengths are inputs of
+// the whole call, complete before the attention kernel lets this one start, so
+// the division of work is computed while that one runs; then the rows of
 // up to kParts parts and their (m, l) are asked for at once, and what is left
 // is one trip to L2 (part after part it was 5.6 us of a 17 us call).
 constexpr int kParts = 20;
 
+// Groups of a launch, of every length; below 2^31 (the host refuses more).
+__host__ __device__ inline uint32_t combine_groups(const TreeParams& p, int rows) {
+  return static_cast<uint32_t>(p.B) * p.Hkv * ((p.G * p.T + rows - 1) / rows);
+}
+
 template <int D, int ROWS, int TR>
 __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant__ TreeParams p) {
   const int lane = threadIdx.x & 31;
-  const uint32_t rows = static_cast<uint32_t>(p.G) * p.T;
-  const uint32_t w = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const uint32_t bg = w / rows;
-  const int i = static_cast<int>(w - bg * rows);
-  const int b = static_cast<int>(bg / p.Hkv);
-  const int g = static_cast<int>(bg) - b * p.Hkv;
-  const int t = i / p.G, h = g * p.G + i % p.G;
-  const TreeSched<TR, ROWS> sched(p);
-  const TreeElem e = b < p.B ? sched.elem(b) : TreeElem{0, 0};
-  const int mb = i / ROWS, row = i % ROWS;
-  const uint32_t nt = static_cast<uint32_t>((e.n + TR - 1) / TR);
+  TreeSched<TR, ROWS> sched(p);
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);  // of the block of rows
+  int b = 0, g = 0, mb = 0;
+  uint32_t x0 = 0, nt = 0;  // the group's tiles
+  TreeElem e{0, 0};
+  if (combine_groups(p, ROWS) <= static_cast<uint32_t>(p.grid)) {
+    const int mbs = (p.G * p.T + ROWS - 1) / ROWS, bg = static_cast<int>(blockIdx.x) / mbs;
+    mb = static_cast<int>(blockIdx.x) - bg * mbs;
+    b = bg / p.Hkv;
+    g = bg - b * p.Hkv;
+    while (b >= sched.b0 + 32) sched.window(sched.b0 + 32, __shfl_sync(0xffffffffu, sched.upto, 31));
+    e = sched.elem(b);
+    nt = static_cast<uint32_t>((e.n + TR - 1) / TR);
+    x0 = __shfl_sync(0xffffffffu, sched.upto - sched.tiles, b - sched.b0) + static_cast<uint32_t>(g * sched.blocks(e) + mb) * nt;
+  } else {
+    const uint32_t cut = sched.begin(blockIdx.x + 1);
+    if (cut < sched.total) {
+      const TreePiece pc = piece_at<TR, ROWS>(sched, cut, cut + 1);
+      x0 = cut - pc.t0;
+      if (pc.t0 > 0 && sched.begin(blockIdx.x) <= x0) {
+        b = pc.b;
+        g = pc.g;
+        mb = pc.mb;
+        e = pc.e;
+        nt = static_cast<uint32_t>(pc.nt);
+      }
+    }
+  }
+  const int i = mb * ROWS + row, t = i / p.G, h = g * p.G + i % p.G;
   int c0 = 0, c1 = 0;
-  if (t < e.cnt) {
-    const uint32_t x0 = sched.first_tile(b) + static_cast<uint32_t>(g * sched.blocks(e) + mb) * nt;
+  if (row < ROWS && t < e.cnt) {
     c0 = static_cast<int>(sched.owner(x0));
     c1 = static_cast<int>(sched.owner(x0 + nt - 1));
   }
@@ -777,9 +803,10 @@ cudaError_t launch_mma(const TreeParams* p, int device, cudaStream_t stream) {
 
 template <int D, int ROWS, int TR>
 cudaError_t launch_combine(const TreeParams* p, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(p->B) * p->Hkv * p->G * p->T;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  const int rows = p->G * p->T < ROWS ? p->G * p->T : ROWS;
+  const uint32_t groups = combine_groups(*p, ROWS), grid = static_cast<uint32_t>(p->grid);
+  cfg.gridDim = dim3(groups < grid ? groups : grid, static_cast<unsigned>((rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

@@ -31,52 +31,87 @@ __device__ __forceinline__ TreeElem tree_elem(const TreeParams& p, int b, bool* 
   return e;
 }
 
-// Called by whole warps; every lane gets the result.  Lane j keeps element
-// j's lengths (of the first 32; a larger batch is read again, 32 at a time).
-// The host refuses calls that could have 2^31 tiles, so 32 bits do.
+// Tiles of 32 elements, a window of the batch: lane j keeps element b0 + j's
+// lengths.  Called by whole warps; every lane gets the result.  The host refuses
+// calls that could have 2^31 tiles, so 32 bits do.
 template <int TR, int ROWS>
-struct TreeSched {
+struct TreeLens {
   const TreeParams& p;
-  TreeElem mine;         // of element `lane`
-  uint32_t tiles, upto;  // its tiles; the tiles of elements 0 .. lane
-  uint32_t total;
-  uint32_t grid;         // CTAs that have tiles
-  uint32_t share, more;  // the first `more` CTAs have share + 1 tiles, the others share
-  uint32_t per, nt1;     // groups of one length (one element): CTAs and tiles of each; per 0: as above
+  TreeElem mine;         // of element b0 + lane
+  uint32_t tiles, upto;  // its tiles; the tiles of all elements up to it
+  int b0;
+  uint32_t base;  // the tiles of the elements before the window
 
   // blocks of query rows of a KV head
   __device__ __forceinline__ int blocks(const TreeElem& e) const { return (e.cnt * p.G + ROWS - 1) / ROWS; }
-  __device__ __forceinline__ TreeElem elem_of_lane(int b0) const {
-    const int b = b0 + static_cast<int>(threadIdx.x & 31);
+  __device__ __forceinline__ TreeElem elem_of_lane(int first) const {
+    const int b = first + static_cast<int>(threadIdx.x & 31);
     bool bad = false;
     return b < p.B ? tree_elem(p, b, &bad) : TreeElem{0, 0};
   }
   __device__ __forceinline__ uint32_t tiles_of(const TreeElem& e) const {
     return static_cast<uint32_t>((e.n + TR - 1) / TR) * static_cast<uint32_t>(p.Hkv * blocks(e));
   }
-  static __device__ __forceinline__ uint32_t scan(uint32_t x) {
+  __device__ __forceinline__ void window(int first, uint32_t before) {
+    b0 = first;
+    base = before;
+    mine = elem_of_lane(first);
+    tiles = tiles_of(mine);
+    upto = tiles;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-    return x;
+    upto += before;
   }
-  __device__ __forceinline__ explicit TreeSched(const TreeParams& prm) : p(prm) {
-    mine = elem_of_lane(0);
-    tiles = tiles_of(mine);
-    upto = scan(tiles);
-    total = __shfl_sync(0xffffffffu, upto, 31);
-    for (int b0 = 32; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, tiles_of(elem_of_lane(b0)));
-    grid = min(static_cast<uint32_t>(p.grid), max(total, 1u));
+  __device__ __forceinline__ TreeLens(const TreeParams& prm, int first, uint32_t before) : p(prm) { window(first, before); }
+  // element b of the window
+  __device__ __forceinline__ TreeElem elem(int b) const {
+    TreeElem e;
+    e.n = __shfl_sync(0xffffffffu, mine.n, b - b0);
+    e.cnt = __shfl_sync(0xffffffffu, mine.cnt, b - b0);
+    return e;
+  }
+  // the element that tile x belongs to, and its first tile; x is not before the
+  // window, which moves on to it
+  __device__ __forceinline__ void locate(uint32_t x, int* b, uint32_t* first) {
+    unsigned hit = __ballot_sync(0xffffffffu, x < upto);
+    while (!hit && b0 + 32 < p.B) {
+      window(b0 + 32, __shfl_sync(0xffffffffu, upto, 31));
+      hit = __ballot_sync(0xffffffffu, x < upto);
+    }
+    const int src = hit ? __ffs(hit) - 1 : 0;
+    *b = b0 + src;
+    *first = __shfl_sync(0xffffffffu, upto - tiles, src);
+  }
+};
+
+template <int TR, int ROWS>
+struct TreeSched : TreeLens<TR, ROWS> {
+  uint32_t total;
+  uint32_t grid;         // CTAs that have tiles
+  uint32_t share, more;  // the first `more` CTAs have share + 1 tiles, the others share
+  uint32_t per, nt1;     // groups of one length (one element): CTAs and tiles of each; per 0: as above
+
+  __device__ __forceinline__ explicit TreeSched(const TreeParams& prm) : TreeLens<TR, ROWS>(prm, 0, 0u) {
+    total = __shfl_sync(0xffffffffu, this->upto, 31);
+    if (prm.B > 32) {
+      uint32_t mine = 0u;
+#pragma unroll 4
+      for (int b = 32; b < prm.B; b += 32) mine += this->tiles_of(this->elem_of_lane(b));
+      total += __reduce_add_sync(0xffffffffu, mine);
+    }
+    grid = min(static_cast<uint32_t>(prm.grid), max(total, 1u));
     per = 0;
-    if (p.B == 1) {
+    nt1 = 1;
+    if (prm.B == 1) {
       // as many CTAs for each group, so that no run spans two groups (a second
       // start and merge in one CTA costs more than the few CTAs left over: one
       // token at 4097 rows, 144 CTAs against 148)
-      const TreeElem e = elem(0);
-      const uint32_t groups = static_cast<uint32_t>(p.Hkv * blocks(e));
+      const TreeElem e = this->elem(0);
+      const uint32_t groups = static_cast<uint32_t>(prm.Hkv * this->blocks(e));
       nt1 = static_cast<uint32_t>((e.n + TR - 1) / TR);
       if (groups > 0 && grid >= groups) {
         per = min(grid / groups, nt1);
@@ -85,17 +120,6 @@ struct TreeSched {
     }
     share = total / grid;
     more = total - share * grid;
-  }
-  __device__ __forceinline__ TreeElem elem(int b) const {
-    TreeElem e;
-    if (b < 32) {
-      e.n = __shfl_sync(0xffffffffu, mine.n, b);
-      e.cnt = __shfl_sync(0xffffffffu, mine.cnt, b);
-    } else {
-      bool bad = false;
-      e = tree_elem(p, b, &bad);
-    }
-    return e;
   }
   // (a group has at most 2^23 tiles of 128 rows, and `per` is at most the SMs)
   __device__ __forceinline__ uint32_t begin(uint32_t cta) const {
@@ -115,59 +139,29 @@ struct TreeSched {
     if (j + 1 < per && nt1 * (j + 1) / per <= r) ++j;
     return g * per + j;
   }
-  // the element that tile x belongs to, and its first tile
-  __device__ __forceinline__ void locate(uint32_t x, int* b, uint32_t* first) const {
-    unsigned hit = __ballot_sync(0xffffffffu, x < upto);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      *b = src;
-      *first = __shfl_sync(0xffffffffu, upto - tiles, src);
-      return;
-    }
-    uint32_t base = __shfl_sync(0xffffffffu, upto, 31);
-    *b = 0;
-    *first = 0;
-    for (int b0 = 32; b0 < p.B; b0 += 32) {
-      const uint32_t tl = tiles_of(elem_of_lane(b0)), up = scan(tl);
-      hit = __ballot_sync(0xffffffffu, x < base + up);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        *b = b0 + src;
-        *first = __shfl_sync(0xffffffffu, base + up - tl, src);
-        return;
-      }
-      base += __shfl_sync(0xffffffffu, up, 31);
-    }
-  }
-  // the first tile of element b
-  __device__ __forceinline__ uint32_t first_tile(int b) const {
-    if (b < 32) return __shfl_sync(0xffffffffu, upto - tiles, b);
-    uint32_t base = __shfl_sync(0xffffffffu, upto, 31);
-    for (int b0 = 32; b0 < b; b0 += 32) {
-      const uint32_t tl = tiles_of(elem_of_lane(b0));
-      base += __reduce_add_sync(0xffffffffu, b0 + static_cast<int>(threadIdx.x & 31) < b ? tl : 0u);
-    }
-    return base;
-  }
 };
 
 // A run's part of one group: tiles [t0, t1) of its nt.
 struct TreePiece {
   int b, g, mb, t0, t1, nt;
   TreeElem e;
+  int b0;  // the window that it was found in
+  uint32_t base;
 };
 
 // The piece that holds tile x of a run that ends at xend.
 template <int TR, int ROWS>
-__device__ __forceinline__ TreePiece piece_at(const TreeSched<TR, ROWS>& sched, uint32_t x, uint32_t xend) {
+__device__ __forceinline__ TreePiece piece_at(TreeLens<TR, ROWS>& lens, uint32_t x, uint32_t xend) {
   TreePiece pc;
   uint32_t first;
-  sched.locate(x, &pc.b, &first);
-  pc.e = sched.elem(pc.b);
+  lens.locate(x, &pc.b, &first);
+  pc.e = lens.elem(pc.b);
+  pc.b0 = lens.b0;
+  pc.base = lens.base;
   pc.nt = (pc.e.n + TR - 1) / TR;
   const uint32_t rel = x - first, nt = static_cast<uint32_t>(pc.nt);
   const int grp = static_cast<int>(rel / nt);
-  const int mbs = sched.blocks(pc.e);
+  const int mbs = lens.blocks(pc.e);
   pc.g = mbs == 1 ? grp : grp / mbs;
   pc.mb = grp - pc.g * mbs;
   pc.t0 = static_cast<int>(rel - static_cast<uint32_t>(grp) * nt);
@@ -178,9 +172,9 @@ __device__ __forceinline__ TreePiece piece_at(const TreeSched<TR, ROWS>& sched, 
 // As calls, not inlined: each role of the tcgen05 kernel walks the run, and with
 // the walk in each of them its loops lie far apart in the instruction caches.
 template <int TR, int ROWS>
-__device__ __noinline__ TreePiece tree_piece(const TreeParams& p, uint32_t x) {
-  const TreeSched<TR, ROWS> sched(p);
-  return piece_at(sched, x, sched.begin(blockIdx.x + 1));
+__device__ __noinline__ TreePiece tree_piece(const TreeParams& p, uint32_t x, uint32_t xend, int b0, uint32_t base) {
+  TreeLens<TR, ROWS> lens(p, b0, base);
+  return piece_at(lens, x, xend);
 }
 template <int TR, int ROWS>
 __device__ __noinline__ uint2 tree_run(const TreeParams& p) {
@@ -193,17 +187,19 @@ template <int TR, int ROWS>
 struct TreeWalk {
   const TreeParams& p;
   uint32_t x, xend;
+  int b0 = 0;
+  uint32_t base = 0;
   __device__ __forceinline__ explicit TreeWalk(const TreeParams& prm) : p(prm) {
     const uint2 run = tree_run<TR, ROWS>(prm);
     x = run.x;
     xend = run.y;
   }
-  // tiles of the run; before the first next()
-  __device__ __forceinline__ uint32_t run_tiles() const { return xend - x; }
   __device__ __forceinline__ bool next(TreePiece* pc) {
     if (x >= xend) return false;
-    *pc = tree_piece<TR, ROWS>(p, x);
+    *pc = tree_piece<TR, ROWS>(p, x, xend, b0, base);
     x += pc->t1 - pc->t0;
+    b0 = pc->b0;
+    base = pc->base;
     return true;
   }
 };

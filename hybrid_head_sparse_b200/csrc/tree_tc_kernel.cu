@@ -368,7 +368,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 2^(e - top), e <= top, as f16; NaN for scale byte 255.  (A row that is not there has any factor.)
+// 2^(e - top), e <= top, as f16; NaN for scale byte 255.
 __device__ __forceinline__ uint32_t factor_f16(int e, int top) {
   const int x = 15 + e - top;  // the biased exponent
   return e == 255 ? 0x7fffu : x > 0 ? static_cast<uint32_t>(x) << 10 : x > -10 ? 0x200u >> -x : 0u;
@@ -427,6 +427,7 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const bool have = (off[k] & 1) == 0;
+      if (!have) kb[k] = vb[k] = 0u;
       if (have && kb[k] != 255u) {
         kt = max(kt, kb[k]);
         kl = max(kl, 255u - kb[k]);

@@ -592,6 +592,29 @@ def test_tree_many_elements(lyc, e4m3, T, hq, cap, page):
     check_tree(lyc, cache, q, n, t_len, mask, what="many")
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,hq,hkv,B", [(1, 4, 2, 300), (12, 4, 1, 300), (3, 2, 2, 90)])
+def test_tree_large_batches(lyc, e4m3, T, hq, hkv, B):
+    """Far more groups than CTAs, a few of them cut over several: lengths of zero to
+    200, and some of thousands at the ends and edges of the windows of 32 elements."""
+    rng = np.random.default_rng(B + T)
+    page, cap = 16, 6000
+    t_len = [int(x) for x in rng.integers(0, T + 1, B)]
+    n = [int(rng.integers(c, 200)) for c in t_len]
+    for b, x in ((0, 5000), (31, 6000), (32, 3000), (33, 1), (64, 4096), (B - 1, 5999)):
+        t_len[b], n[b] = min(T, x), x
+    pages = [-(-x // page) for x in n]
+    table = torch.zeros((B, cap // page), dtype=torch.int32)
+    order, at = rng.permutation(sum(pages)), 0
+    for b in range(B):
+        table[b, : pages[b]] = torch.from_numpy(order[at: at + pages[b]].astype(np.int32))
+        at += pages[b]
+    proto = fill(lyc, 1, hkv, 128, sum(pages) * page, page, e4m3, seed=B)
+    k, v, ks, vs, _ = proto.tensors
+    cache = lyc.KvCache(k, v, ks, vs, block_table=table.cuda())
+    check_tree(lyc, cache, randn(T, B, T, hq, 128), n, t_len, random_tree(rng, B, T), what="large batch")
+
+
 @pytest.mark.parametrize("T,page", [(3, 0), (3, 16), (20, 0), (20, 16)])
 def test_tree_scales_of_every_size(lyc, T, page):
     """Scales far from 1 in K and V: V's to 2^23 apart over few query rows (fp16
