@@ -3,12 +3,13 @@
 // captured graph serves every length up to the cache's capacity).
 //
 // A group is one (element b, KV head g, block mb of its G * t_len[b] query
-// rows); it has nt(b) = ceil(n[b] / tile rows) tiles of the cache.  The tiles of all groups, in order, are cut into `grid`
-// equal runs, one for each CTA (with fewer tiles than CTAs, the CTAs past the
-// last tile have none: a CTA inside a cut group always has a slot).  A run holds whole groups, whose outputs its
-// CTA writes, and at most two cut ones: the end of a group begun by an earlier
-// CTA (partial slot 2c) and the start of one that a later CTA goes on with
-// (slot 2c + 1).  The combine launch merges a cut group's slots.
+// rows); it has nt(b) = ceil(n[b] / tile rows) tiles of the cache.  The tiles of
+// all groups, in order, are cut into `grid` equal runs, one for each CTA (with
+// fewer tiles than CTAs, the CTAs past the last tile have none: a CTA inside a cut
+// group always has a slot).  A run holds whole groups, whose outputs its CTA
+// writes, and at most two cut ones: the end of a group begun by an earlier CTA
+// (partial slot 2c) and the start of one that a later CTA goes on with (slot 2c +
+// 1).  The combine launch merges a cut group's slots.
 #pragma once
 #include <stdint.h>
 

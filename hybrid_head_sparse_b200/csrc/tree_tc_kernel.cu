@@ -17,10 +17,10 @@
 // whose rows is a query does nothing but keep the barriers going.
 //
 // A block of 64 query rows or fewer has them twice over in the 128 lanes, and each
-// copy takes half of a key half (its P is zero elsewhere), so the
-// exponentials are spread over all the schedulers instead of staying with the
-// warps of the first rows.  The copies are parts like those of other CTAs, merged
-// with them, or in the CTA for a whole group.
+// copy takes half of a key half (its P is zero elsewhere), so the exponentials are
+// spread over all the schedulers instead of staying with the warps of the first
+// rows.  The copies are parts like those of other CTAs, merged with them, or in the
+// CTA for a whole group.
 //
 // bf16 rows: K and V tiles are read by the tensor core where TMA puts them.
 // Masked rows have P = 0, and 0 * NaN would reach every row, so in the tiles
@@ -31,18 +31,17 @@
 // e4m3 rows become f16 tiles on their way: code * 2^(e - E), E the largest e of the
 // tile's rows, so the products run in f16.  2^E of K is a factor of the tile's
 // logits; V's goes into the exponent, p' = 2^(z + E - m'), m' the running maximum of
-// z + E, and the sum
-// takes p' 2^-E.  That is exact while the tile's e are within 15 of each other; where
-// they are not (a row of zeros; a drafted row that nobody has written or sees), the
-// tile is the codes alone and the softmax warps apply each row's scales.  A query
-// row becomes f16 as in tree_mma_kernel.cu.  Three warps find the rows of coming
-// tiles and their scales; eight producer warps copy the codes in, convert them
-// (two instructions for two codes) and store them.
+// z + E, and the sum takes p' 2^-E.  That is exact while the tile's e are within 15
+// of each other; where they are not (a row of zeros; a drafted row that nobody has
+// written or sees), the tile is the codes alone and the softmax warps apply each
+// row's scales.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps find
+// the rows of coming tiles and their scales; eight producer warps copy the codes
+// in, convert them (two instructions for two codes) and store them.
 //
 // Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 92 to
 // 98 us, 5.5 to 5.8 TB/s, 0.84 to 0.89 of the copy rate: HBM, and the
 // exponentials (1024 cycles of a tile's 2600).  4 x 16 nodes over up to 65536
-// e4m3 rows each: 166 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 117.
+// e4m3 rows each: 166 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 107 to 140.
 // There a tile takes 3200 cycles against the 1300 of its bytes: 1000 of the tensor
 // cores, 1800 of shared memory, and the softmax warps' chain of latencies, which
 // twenty warps on an SM stretch to 2500.  Slower were: bf16 tiles, codes converted by
