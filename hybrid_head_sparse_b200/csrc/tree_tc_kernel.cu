@@ -20,7 +20,7 @@
 // copy takes half of a key half (its P is zero elsewhere), so the exponentials are
 // spread over all the schedulers instead of staying with the warps of the first
 // rows.  The copies are parts like those of other CTAs, merged with them, or in the
-// CTA for a whole group.
+// CTA for a whole group, which has them only where it is long.
 //
 // bf16 rows: K and V tiles are read by the tensor core where TMA puts them.
 // Masked rows have P = 0, and 0 * NaN would reach every row, so in the tiles
@@ -824,6 +824,7 @@ __device__ __noinline__ bool merge_copies(const CopyMerge& m, uint32_t phase) {
   return true;
 }
 constexpr uint32_t kMergeWaits = 5;
+constexpr int kMergeTiles = 16;  // of a whole group: fewer are not worth the merge, 11000 to 16000 cycles
 
 // A tile whose rows have their own scales: n columns of logits from `col` on become
 // z + e in log2 units (e of V), -inf where `vis` is not set.
@@ -886,7 +887,8 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
   int t = 0, piece = 0;
   uint32_t together = 0;  // times that all softmax warps have waited for one another
   while (walk.next(&pc)) {
-    const int copies = tree_copies(pc.e.cnt * p.G - pc.mb * kRows), span = kRows / copies;
+    const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
+    const int copies = whole && pc.nt < kMergeTiles ? 1 : tree_copies(pc.e.cnt * p.G - pc.mb * kRows), span = kRows / copies;
     const int copy = i / span;
     const int row = pc.mb * kRows + i - copy * span;
     const int node = row / p.G, head = pc.g * p.G + row % p.G;
@@ -897,19 +899,33 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
     float row_log2 = p.scale_log2;  // F8: with the row's power of two
     if (warp_live) {
       const unsigned char* src = p.q + 2 * (pc.b * p.q_batch + node * p.q_token + head * p.q_head);
+      uint4 mine[8];
+#pragma unroll
+      for (int c8 = 0; c8 < 8; ++c8) {
+        mine[c8] = make_uint4(0u, 0u, 0u, 0u);
+        if (live) mine[c8] = *reinterpret_cast<const uint4*>(src + (hf * 8 + c8) * 16);
+      }
       float f1 = 1.f, f2 = 1.f;
       if (C::F8) {
         // as f16, scaled by a power of two to below 2 (exact for elements down to 2^-14
         // of the row's largest, half of 2^-24 off below)
         uint32_t mx = 0u;
-        if (live)
-#pragma unroll 4
-          for (int ch = 0; ch < 16; ++ch) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src + ch * 16);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        auto most = [&](const uint4& v) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-          }
+          for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+        };
+        uint4 other[8];  // all of the row is asked for at once
+#pragma unroll
+        for (int c8 = 0; c8 < 8; ++c8) {
+          other[c8] = make_uint4(0u, 0u, 0u, 0u);
+          if (live) other[c8] = *reinterpret_cast<const uint4*>(src + ((1 - hf) * 8 + c8) * 16);
+        }
+#pragma unroll
+        for (int c8 = 0; c8 < 8; ++c8) {
+          most(mine[c8]);
+          most(other[c8]);
+        }
         int ex = static_cast<int>(mx >> 7);  // biased exponent of the row's largest element
         if (ex == 0 || ex == 255) ex = 127;
         // it comes off in two factors: 2^-(ex - 127) may be out of fp32's range
@@ -921,8 +937,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
 #pragma unroll
       for (int c8 = 0; c8 < 8; ++c8) {
         const int ch = hf * 8 + c8;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (live) v = *reinterpret_cast<const uint4*>(src + ch * 16);
+        uint4 v = mine[c8];
         if (C::F8) {
           v.x = tc_pack_f16(bf16lo(v.x) * f1 * f2, bf16hi(v.x) * f1 * f2);
           v.y = tc_pack_f16(bf16lo(v.y) * f1 * f2, bf16hi(v.y) * f1 * f2);
@@ -1091,7 +1106,6 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
     *ml_of(1 - hf) = make_float2(m_used, lsum);
     tc_arrive_warp(br.ml_ready);
     if (!tc_wait_warp(br.ml_ready, together++ & 1, sh.abort, p.status)) return;
-    const bool whole = pc.t0 == 0 && pc.t1 == pc.nt;
     const bool merge = whole && copies > 1;
     if (warp_live || merge) {
       const float2 own = make_float2(m_used, lsum), other = *ml_of(hf);
