@@ -31,7 +31,7 @@
 // e4m3 rows become f16 tiles on their way: code * 2^(e - E), E the largest e of the
 // tile's rows, so the products run in f16.  2^E of K is a factor of the tile's
 // logits; V's goes into the exponent, p' = 2^(z + E - m'), m' the running maximum of
-// z + E, and the sum takes p' 2^-E.  That is exact while the tile's e are within 15
+// z + E, and the sum takes p' 2^-E.  That is exact while the tile's e are within 14
 // of each other; where they are not (a row of zeros; a drafted row that nobody has
 // written or sees), the tile is the codes alone and the softmax warps apply each
 // row's scales.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps find
@@ -367,12 +367,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 2^(e - top), e <= top, as f16; NaN for scale byte 255.
-__device__ __forceinline__ uint32_t factor_f16(int e, int top) {
-  const int x = 15 + e - top;  // the biased exponent
-  return e == 255 ? 0x7fffu : x > 0 ? static_cast<uint32_t>(x) << 10 : x > -10 ? 0x200u >> -x : 0u;
-}
-
 // What is known of a row of a tile.
 struct RowInfo {
   long long off;    // of its codes in K and in V; odd: no such row, zeros
@@ -421,36 +415,36 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
     }
   };
   auto put = [&](int t) {
-    // the tile's largest scales and 255 less its smallest (a NaN row's are left out)
-    uint32_t kt = 0u, vt = 0u, kl = 0u, vl = 0u;
+    // the tile's largest scales, as byte + 1, so that NaN rows' and those of rows that
+    // are not there count as 0
+    uint32_t kk[4], vv[4], kt = 0u, vt = 0u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const bool have = (off[k] & 1) == 0;
-      if (!have) kb[k] = vb[k] = 0u;
-      if (have && kb[k] != 255u) {
-        kt = max(kt, kb[k]);
-        kl = max(kl, 255u - kb[k]);
-      }
-      if (have && vb[k] != 255u) {
-        vt = max(vt, vb[k]);
-        vl = max(vl, 255u - vb[k]);
-      }
+      const uint32_t have = (off[k] & 1) ? 0u : 255u;
+      kk[k] = (kb[k] + 1u) & have;
+      vv[k] = (vb[k] + 1u) & have;
+      kt = max(kt, kk[k]);
+      vt = max(vt, vv[k]);
     }
     kt = __reduce_max_sync(0xffffffffu, kt);
     vt = __reduce_max_sync(0xffffffffu, vt);
-    kl = __reduce_max_sync(0xffffffffu, kl);
-    vl = __reduce_max_sync(0xffffffffu, vl);
-    // codes are multiples of 2^-9, f16's last place is 2^-24
-    const bool own = kt + kl > 255u + 15u || vt + vl > 255u + 15u;
-    if (own) kt = vt = 127u;
+    // within 2^14 every factor is a normal f16, and codes (multiples of 2^-9) times it are exact
+    bool apart = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) apart |= (kk[k] && kk[k] + 14u < kt) || (vv[k] && vv[k] + 14u < vt);
+    const bool own = __any_sync(0xffffffffu, apart);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int ke = own && kb[k] != 255u ? 127 : kb[k], ve = own && vb[k] != 255u ? 127 : vb[k];
+      uint32_t kf = own || kk[k] == 0u ? 15u << 10 : (15u + kk[k] - kt) << 10;
+      uint32_t vf = own || vv[k] == 0u ? 15u << 10 : (15u + vv[k] - vt) << 10;
+      if (kb[k] == 255u) kf = 0x7fffu;  // NaN (harmless where the row is not there: it is not seen, and V's is cleared)
+      if (vb[k] == 255u) vf = 0x7fffu;
       *reinterpret_cast<uint4*>(&info[(t % kInfoRing) * kRows + 32 * k]) =
-          make_uint4(static_cast<uint32_t>(off[k]), static_cast<uint32_t>(off[k] >> 32),
-                     factor_f16(ke, kt) | (factor_f16(ve, vt) << 16), kb[k] | (vb[k] << 8));
+          make_uint4(static_cast<uint32_t>(off[k]), static_cast<uint32_t>(off[k] >> 32), kf | (vf << 16), kb[k] | (vb[k] << 8));
     }
-    if (lane == 0) *reinterpret_cast<uint2*>(sh.top + (t % kOkRing) * 2) = make_uint2(kt | (own ? kOwn : 0u), vt);
+    if (lane == 0)
+      *reinterpret_cast<uint2*>(sh.top + (t % kOkRing) * 2) =
+          own ? make_uint2(127u | kOwn, 127u) : make_uint2(max(kt, 1u) - 1u, max(vt, 1u) - 1u);
     tc_arrive_warp(&br.info_full[t % kInfoRing]);
   };
   ask();
