@@ -152,10 +152,10 @@ int sm_count(int device) {
 // The most query rows of a KV head that the mma.sync kernel takes where the tcgen05
 // kernel could.  Times in us, 32/8 heads of 128, over 131072 rows, 4 x 8192, 2048, 16 x
 // 1024 and 32 x 300:
-//   bf16, 16 rows   mma.sync  87   33  10.5  23  25
-//   bf16, 32 rows   mma.sync  99   43  14    35  42   tcgen05  90  35  15  30  43
-//   e4m3, 32 rows   mma.sync 121   42  15    32  37   tcgen05 106  49  20  42  60
-//   e4m3, 36 rows   mma.sync 214   62  16    51  57   tcgen05 108  50  22  44  62
+//   bf16, 16 rows   mma.sync  86   32  10   23  24
+//   bf16, 32 rows   mma.sync  99   43  14   35  42   tcgen05  90  33  14  29  33
+//   e4m3, 32 rows   mma.sync 122   44  15   32  36   tcgen05 106  48  20  41  49
+//   e4m3, 36 rows   mma.sync 214   62  16   51  57   tcgen05 108  50  21  43  50
 // (mma.sync has blocks of 16 or 32 rows, so more read the cache again; the capacity
 // that the host knows says little of the lengths.)
 constexpr int mma_most_rows(int cache_type) { return cache_type == LYC_CACHE_BF16 ? 16 : 32; }

@@ -41,7 +41,7 @@
 // Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 92 to
 // 98 us, 5.5 to 5.8 TB/s, 0.84 to 0.89 of the copy rate: HBM, and the
 // exponentials (1024 cycles of a tile's 2600).  4 x 16 nodes over up to 65536
-// e4m3 rows each: 166 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 107 to 140.
+// e4m3 rows each: 165 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 114 to 137.
 // There a tile takes 3200 cycles against the 1300 of its bytes: 1000 of the tensor
 // cores, 1800 of shared memory, and the softmax warps' chain of latencies, which
 // twenty warps on an SM stretch to 2500.  Slower were: bf16 tiles, codes converted by
