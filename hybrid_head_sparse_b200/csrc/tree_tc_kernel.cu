@@ -32,9 +32,11 @@
 // tile's rows, so the products run in f16.  2^E of K is a factor of the tile's
 // logits; V's goes into the exponent, p' = 2^(z + E - m'), m' the running maximum of
 // z + E, and the sum takes p' 2^-E.  That is exact while the tile's e are within 14
-// of each other; where they are not (a row of zeros; a drafted row that nobody has
-// written or sees), the tile is the codes alone and the softmax warps apply each
-// row's scales.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps find
+// of each other, and V's are held within 6, so that p' of a row far below E does not
+// fall out of f16's range (at 14, a tail of 65536 rows 2^-18 below the top one was
+// lost beside a row of negligible probability 2^14 larger).  Where they are not (a row
+// of zeros; a drafted row that nobody has written or sees), the tile is the codes
+// alone and the softmax warps apply each row's scales.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps find
 // the rows of coming tiles and their scales; eight producer warps copy the codes
 // in, convert them (two instructions for two codes) and store them.
 //
@@ -76,6 +78,22 @@ constexpr int kFinders = 3;    // warps that find rows, every third tile each
 constexpr int kUnits = 4;      // 4-row units that a producer warp converts at a time
 constexpr int kSide = kProducers / 2;
 constexpr int kGroups = 32 / (kSide * kUnits);  // of a warp's units of a tile
+
+// How far z may grow (log2 units) before the running maximum moves, and where a
+// probability at the maximum lies.  f16 (e4m3 rows) is used from the top, 2^15.9 of
+// 65504; it ends at 2^-24, so a probability is off by at most 2^-36 of the tile's
+// largest times its largest scale of V.  Rows of up to kApartV octaves share a tile's
+// scale: that is 2^-30 of the largest probability * scale of a row.  Beyond that they
+// keep their own.  (4 x 16 nodes over up to 65536 rows: 164.8 us, as with a range of 8 and
+// an apartness of 14; a range of 4 took 168.5, an apartness of 5, which ordinary rows
+// of V reach, 4 us more over 512 rows.  Where every tile's rows are further apart, 355.)
+template <bool F8>
+struct TcRange {
+  static constexpr float kLag = F8 ? 4.9f : 8.f;
+  static constexpr float kTop = F8 ? 11.f : 0.f;
+};
+constexpr uint32_t kApartK = 14;  // every factor of a row is a normal f16, and codes (multiples of 2^-9) times it exact
+constexpr uint32_t kApartV = 6;
 
 template <bool F8_>
 struct TcCfg {
@@ -428,10 +446,9 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
     }
     kt = __reduce_max_sync(0xffffffffu, kt);
     vt = __reduce_max_sync(0xffffffffu, vt);
-    // within 2^14 every factor is a normal f16, and codes (multiples of 2^-9) times it are exact
     bool apart = false;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) apart |= (kk[k] && kk[k] + 14u < kt) || (vv[k] && vv[k] + 14u < vt);
+    for (int k = 0; k < 4; ++k) apart |= (kk[k] && kk[k] + kApartK < kt) || (vv[k] && vv[k] + kApartV < vt);
     const bool own = __any_sync(0xffffffffu, apart);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -966,7 +983,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
         vis = live ? seen_bits(p, pc, node, kb) & there : 0ull;
       }
       // F8: the tile's K scale is the logit's, its V scale is taken into the exponent
-      // (p' = 2^(z + e - m'), and the sum takes p' 2^-e), f16's range from the top
+      // (p' = 2^(z + e - m'), and the sum takes p' 2^-e)
       float per_s = p.scale_log2, v_exp = 0.f, v_inv = 1.f;
       if (C::F8) {
         per_s = fminf(fmaxf(row_log2 * __uint_as_float(max(top.x & 255u, 1u) << 23), 1.17549435e-38f), 3.4e38f);
@@ -1022,7 +1039,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           }
         }
         const float mx = fmaf(mraw, per_s, v_exp);
-        const bool grow = mx > m_used + 8.f;
+        const bool grow = mx > m_used + TcRange<C::F8>::kLag;
         const bool rescale = grow && m_used != NEG;
         if (__any_sync(FULL, rescale)) {
           if (!tc_wait_warp(&br.pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, sh.abort, p.status)) return;
@@ -1040,7 +1057,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
           lsum *= f;
         }
         if (grow) m_used = mx;
-        const float neg = (m_used == NEG ? 0.f : -m_used) + (C::F8 ? v_exp + 6.f : 0.f);
+        const float neg = (m_used == NEG ? 0.f : -m_used) + (C::F8 ? v_exp + TcRange<true>::kTop : 0.f);
         if (__builtin_expect(own, 0)) lsum += own_sum(ts + k0, 64 / copies, own_row, neg);
         const f2_t neg2 = f2(neg, neg), sl2 = f2(per_s, per_s);
         f2_t sum2 = f2(0.f, 0.f);

@@ -1,0 +1,102 @@
+"""The serving operators on a B200 where their arithmetic is at its limits: the
+bounds of each cache's own roundings (tests/serve_strict.py), probabilities and
+scales that lie far apart, states merged within a block, and bytes of the cache
+that a call may not touch."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import serve_strict as SS
+from tests.serve_oracle import close
+from tests.test_gpu_serve_ops import BF, check_tree, fill, i32, poison_past, randn, random_tree, run_tree, status_word
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lyc():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from hybrid_head_sparse_b200 import lyc as m
+    m.load()
+    return m
+
+
+def strict(lyc, cache, q, n, t_len=None, mask=None, scale=None, what="", lost=SS.LOST):
+    B, T = q.shape[:2]
+    out, st = run_tree(lyc, cache, q, n, t_len, mask, scale)
+    assert st == 0
+    cnt = [T] * B if t_len is None else t_len
+    want, bound = SS.tree(q, cache, n, cnt, mask, q.shape[3]**-0.5 if scale is None else scale, lost)
+    for b in range(B):
+        close(out[b, :cnt[b]], want[b, :cnt[b]].cpu(), bound[b, :cnt[b]].cpu(), f"{what} element {b}")
+        assert bool((out[b, cnt[b]:] == 1234.0).all()), "padding was written"
+    return out
+
+
+def plain_scales(cache):
+    for s in cache.tensors[2:4]:
+        s.view(torch.uint8).fill_(127)
+
+
+def e4m3(x):
+    return torch.tensor(x, device="cuda").to(torch.float8_e4m3fn)
+
+
+# ------------------------------------------------------------------ probabilities
+
+
+def shared_by(lyc, one, B):
+    """B elements that all read the one element of `one`: a block then has many of its
+    tiles, where a single element's are dealt to all blocks."""
+    k, v, ks, vs, _ = (None if x is None else x.view(torch.uint8) for x in one.tensors)
+    wide = [x.expand(B, *x.shape[1:]) for x in (k, v, ks, vs)]
+    return lyc.KvCache(*(x.view(torch.float8_e4m3fn) for x in wide[:2]), *wide[2:])
+
+
+def check_shared(lyc, one, q, n, mask, what):
+    """q of one element, asked for by 150 of them, with q . k as the natural logarithm
+    of 2^(q . k)."""
+    B = 150
+    wide = None if mask is None else mask.expand(B, -1, -1).contiguous()
+    out, st = run_tree(lyc, shared_by(lyc, one, B), q.expand(B, -1, -1, -1), [n] * B, None, wide, scale=math.log(2.0))
+    assert st == 0
+    want, bound = SS.tree(q, one, [n], [q.shape[1]], mask, math.log(2.0))
+    for b in range(B):
+        close(out[b], want[0].cpu(), bound[0].cpu(), f"{what} element {b}")
+
+
+def one_hot(T):
+    q = torch.zeros((1, T, 1, 128), dtype=BF, device="cuda")
+    q[..., 0] = 1.0
+    return q
+
+
+@pytest.mark.parametrize("spread", [5, 6, 7, 14, 15])
+@pytest.mark.parametrize("T,unseen", [(20, False), (40, False), (40, True), (100, False), (100, True)])
+def test_a_tail_beside_a_larger_scale(lyc, T, spread, unseen):
+    """65536 rows, each 2^-18 of the top one's probability, are a fifth of the sum; in
+    the top row's tile a row that hardly counts (2^-60), or that no node sees, has a V
+    scale 2^spread larger.  What it does to the probabilities' range costs nothing."""
+    N, d = 65536 + (64 if unseen else 0), 128
+    n = N + T
+    cache = lyc.KvCache.empty(1, 1, d, rows=n)
+    plain_scales(cache)
+    k, v, _, vs, _ = cache.tensors
+    k[0, 0, :, 0] = e4m3(-18.0)
+    v.copy_(e4m3(1.5).expand(v.shape))
+    v[0, 0, :, 1::2] = e4m3(-1.25)
+    vs.view(torch.uint8).fill_(127 - spread)
+    mask = torch.zeros((1, T, -(-T // 64)), dtype=torch.int64, device="cuda")
+    top, odd = (N - 1, N + 3) if unseen else (70, 3)
+    if not unseen:  # every node sees itself
+        for t in range(T):
+            mask[0, t, t // 64] = 1 << (t % 64) if t % 64 < 63 else -(1 << 63)
+    k[0, 0, top, 0] = e4m3(0.0)
+    v[0, 0, top] = e4m3(1.0)
+    k[0, 0, odd, 0] = e4m3(-60.0)
+    vs.view(torch.uint8)[0, 0, odd] = 127
+    check_shared(lyc, cache, one_hot(T), n, mask, "tail")
