@@ -100,3 +100,27 @@ def test_a_tail_beside_a_larger_scale(lyc, T, spread, unseen):
     k[0, 0, odd, 0] = e4m3(-60.0)
     vs.view(torch.uint8)[0, 0, odd] = 127
     check_shared(lyc, cache, one_hot(T), n, mask, "tail")
+
+
+@pytest.mark.parametrize("T,hq,hkv,d,page,n", [
+    (1, 8, 2, 128, 0, 5000), (1, 8, 2, 64, 16, 5000), (4, 16, 2, 128, 48, 3000), (24, 2, 2, 64, 5, 700),
+    (40, 4, 4, 128, 0, 9000), (20, 8, 2, 128, 16, 3000), (64, 8, 2, 128, 7, 1000), (130, 2, 1, 128, 64, 2500),
+    (70, 8, 4, 64, 0, 900),
+])
+def test_e4m3_probabilities_are_fp16(lyc, T, hq, hkv, d, page, n):
+    """Both kernels over an 8-bit cache, its rows' scales up to 2^8 apart, within
+    fp16's rounding: bf16 probabilities, eight times as coarse, would not be."""
+    B = 3
+    lens = [n, max(T, n // 3), T]
+    cnt = [T, max(1, T - 1), T]
+    cache = fill(lyc, B, hkv, d, n, page, True, seed=T + d)
+    poison_past(cache, lens)
+    q = randn(T, B, T, hq, d)
+    mask = random_tree(np.random.default_rng(T), B, T, empty=(T - 1,) if T > 4 else ())
+    strict(lyc, cache, q, lens, cnt, mask, what="tree")
+    strict(lyc, cache, q, lens, cnt, None, what="chain")
+    # all the rows of V one sign, all of one size: what the bound is for
+    for x in cache.tensors[1:2]:
+        b = x.view(torch.uint8)
+        b &= 0x7F
+    strict(lyc, cache, q * 0.125, lens, cnt, None, what="one sign")
