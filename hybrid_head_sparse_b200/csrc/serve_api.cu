@@ -434,6 +434,7 @@ lyc_status lyc_tree_attention(const lyc_layer_cache* c, const lyc_tree_args* a, 
   p.Hkv = c->num_kv_heads;
   p.G = a->num_q_heads / c->num_kv_heads;
   p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.sum_unit = c->type == LYC_CACHE_E4M3 ? kSumUnitE4m3 : 1.f;
   p.cache = view(c);
   if (s.tc && c->type == LYC_CACHE_BF16) {
     p.box_rows = tree_tc_box_rows(p.cache);

@@ -89,6 +89,13 @@ struct ReadParams {
   CacheView cache;
 };
 
+// Over e4m3 rows a row's part of the softmax's sum is p' 2^-e, where p' = 2^(z + e - m')
+// lies below 2^16 and e is its scale of V, -100 at least (kMinScaleV, the writer's
+// smallest; a smaller one counts as that).  Held as 2^-16 of itself the sum of 2^27 such
+// rows is finite; at e = 120 one row's is 2^-130, a number yet.
+constexpr float kSumUnitE4m3 = 0x1p-16f;
+constexpr uint32_t kMinScaleV = 27;  // 2^-100
+
 struct TreeParams {
   const unsigned char* q;
   unsigned char* out;
@@ -103,6 +110,7 @@ struct TreeParams {
   int32_t grid;
   int32_t box_rows;  // tcgen05 kernel, bf16: rows of one TMA box
   float scale_log2;
+  float sum_unit;    // the sums are held in this: 1, or kSumUnitE4m3
   CacheView cache;
 };
 

@@ -25,7 +25,7 @@
 // (exact for elements down to 2^-14 of the row's largest).  V's scales 2^e_j
 // go into the exponent: p'_j = 2^(z_j + e_j - m'), m' the running maximum of
 // z_j + e_j, so p' stays in f16's range whatever the scales are, and the sum
-// takes p'_j 2^-e_j.  One token over 131072 such rows: 61 us, 0.67 of the floor (8192 x 4:
+// takes p'_j 2^-e_j (kSumUnitE4m3).  One token over 131072 such rows: 61 us, 0.67 of the floor (8192 x 4:
 // 24, 0.43; head_dim 64: 48), bound by instructions and their chains: codes
 // converted by bit moves took 74, 16 rows at a time 66 (32 at a time cost a cache
 // of 300 rows 1 us of 18), 12 warps of half the chunk no less.
@@ -62,7 +62,7 @@ struct TmCfg {
   static constexpr int KPL = (KC + 31) / 32;    // rows a lane looks up
   static constexpr int ST = 3;                  // stages
   static constexpr int WARPB = ST * 8192;       // a warp's ring
-  static constexpr int OFF_SC = NW * WARPB;     // per warp and stage: K factor, V exponent, 2^-exponent
+  static constexpr int OFF_SC = NW * WARPB;     // per warp and stage: K factor, V exponent, factor of the sum
   static constexpr int SCB = F8 ? KC * 12 : 0;
   static constexpr int OFF_OK = OFF_SC + NW * ST * SCB;  // per warp and stage: rows that exist
   static constexpr int OFF_ML = OFF_OK + NW * ST * 8;    // per warp and row: (m, l)
@@ -203,12 +203,11 @@ struct TmLoader {
       const int r = k * 32 + lane;
       if (r < C::KC) {
         const float nan = __uint_as_float(0x7fffffffu);
-        s[r] = kb[k] == 255 ? nan : __uint_as_float(static_cast<uint32_t>(kb[k]) << 23);
-        s[C::KC + r] = vb[k] == 255 ? nan : static_cast<float>(vb[k] - 127);
+        s[r] = kb[k] == 255 ? nan : __uint_as_float(static_cast<uint32_t>(max(kb[k], 1)) << 23);
+        const int v = max(vb[k], static_cast<int>(kMinScaleV));  // (at the load it would wait for that)
+        s[C::KC + r] = v == 255 ? nan : static_cast<float>(v - 127);
         // finite for a NaN row too: its exponent makes p NaN where it is seen, and 0 * NaN is not 0 where not
-        s[2 * C::KC + r] = vb[k] == 255   ? 1.f
-                           : vb[k] == 254 ? __uint_as_float(0x00400000u)
-                                          : __uint_as_float(static_cast<uint32_t>(254 - vb[k]) << 23);
+        s[2 * C::KC + r] = v == 255 ? 1.f : tree_sum_factor(static_cast<uint32_t>(v));
       }
     }
     pending = -1;
@@ -659,7 +658,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) tree_mma_kernel(const __grid_co
       const int i = pc.mb * C::ROWS + row;
       const int t = i / p.G, h = pc.g * p.G + i % p.G;
       if (pc.t0 == 0 && pc.t1 == pc.nt) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = L == 0.f ? 0.f : p.sum_unit / L;
         *reinterpret_cast<uint2*>(p.out + 2 * (pc.b * p.o_batch + t * p.o_token + h * p.o_head + d0)) =
             make_uint2(pack16<false>(acc.x * inv, acc.y * inv), pack16<false>(acc.z * inv, acc.w * inv));
       } else {
@@ -772,7 +771,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const __grid_constant
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const float inv = L == 0.f ? 0.f : p.sum_unit / L;
   unsigned char* dst = p.out + 2 * (b * p.o_batch + t * p.o_token + h * p.o_head + lane * V);
 #pragma unroll
   for (int k = 0; k < V; k += 2)

@@ -208,6 +208,12 @@ struct TreeWalk {
 // How often the tcgen05 kernel's 128 lanes hold the rows of a block.
 __device__ __forceinline__ int tree_copies(int rows) { return rows <= 64 ? 2 : 1; }
 
+// What a p' of a row with this scale byte of V is multiplied by for the sum:
+// 2^-e kSumUnitE4m3 = 2^(111 - byte).
+__device__ __forceinline__ float tree_sum_factor(uint32_t byte) {
+  return __uint_as_float(byte < 238u ? (238u - byte) << 23 : 1u << (260u - byte));
+}
+
 // Does query t of element b see drafted node j (both below its count)?
 __device__ __forceinline__ bool tree_sees(const TreeParams& p, int b, int t, int j) {
   if (!p.mask) return j <= t;

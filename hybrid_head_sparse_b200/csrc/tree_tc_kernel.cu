@@ -31,7 +31,7 @@
 // e4m3 rows become f16 tiles on their way: code * 2^(e - E), E the largest e of the
 // tile's rows, so the products run in f16.  2^E of K is a factor of the tile's
 // logits; V's goes into the exponent, p' = 2^(z + E - m'), m' the running maximum of
-// z + E, and the sum takes p' 2^-E.  That is exact while the tile's e are within 14
+// z + E, and the sum takes p' 2^-E (kSumUnitE4m3).  That is exact while the tile's e are within 14
 // of each other, and V's are held within 6, so that p' of a row far below E does not
 // fall out of f16's range (at 14, a tail of 65536 rows 2^-18 below the top one was
 // lost beside a row of negligible probability 2^14 larger).  Where they are not (a row
@@ -439,6 +439,7 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t have = (off[k] & 1) ? 0u : 255u;
+      vb[k] = max(vb[k], kMinScaleV);  // (here, not at the load: that would wait for it)
       kk[k] = (kb[k] + 1u) & have;
       vv[k] = (vb[k] + 1u) & have;
       kt = max(kt, kk[k]);
@@ -823,7 +824,7 @@ __device__ __noinline__ bool merge_copies(const CopyMerge& m, uint32_t phase) {
           o[4 * q + 3] = fmaf(u.w, f, o[4 * q + 3]);
         }
       }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const float inv = L == 0.f ? 0.f : (C::F8 ? kSumUnitE4m3 : 1.f) / L;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         *reinterpret_cast<uint4*>(m.dst + step * 64 + q * 16) =
@@ -857,7 +858,7 @@ __device__ __noinline__ void own_logits(uint32_t col, int n, const RowInfo* own,
   }
   tc_wait_st();
 }
-// ... and the sum of 2^(z + neg) over them.
+// ... and the sum of 2^(z + neg) over them, in units of 2^16 (kSumUnitE4m3).
 __device__ __noinline__ float own_sum(uint32_t col, int n, const RowInfo* own, float neg) {
   float sum = 0.f;
 #pragma unroll 1
@@ -869,7 +870,7 @@ __device__ __noinline__ float own_sum(uint32_t col, int n, const RowInfo* own, f
     for (int j = 0; j < 16; ++j) {
       const uint32_t v = own[c + j].own >> 8;
       const float ev = v == 255u ? 0.f : static_cast<float>(static_cast<int>(v) - 127);
-      sum += tc_ex2(__uint_as_float(r[0][j]) - ev + neg);
+      sum += tc_ex2(__uint_as_float(r[0][j]) - ev + (neg - 16.f));
     }
   }
   return sum;
@@ -988,7 +989,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       if (C::F8) {
         per_s = fminf(fmaxf(row_log2 * __uint_as_float(max(top.x & 255u, 1u) << 23), 1.17549435e-38f), 3.4e38f);
         v_exp = static_cast<float>(static_cast<int>(top.y) - 127);
-        v_inv = __uint_as_float(top.y == 254u ? 0x00400000u : (254u - top.y) << 23);
+        v_inv = tree_sum_factor(top.y);
       }
       if (warp_live) {
         // both passes read the logits from tensor memory, 32 columns a turn: the
@@ -1125,7 +1126,7 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       const float fa = sa.x == NEG ? 1.f : tc_ex2(sa.x - M);  // 1: the state is zero, or NaN
       const float fb = sb.x == NEG ? 1.f : tc_ex2(sb.x - M);
       const float L = fmaf(sa.y, fa, sb.y * fb);
-      const float unit = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+      const float unit = whole ? (L == 0.f ? 0.f : p.sum_unit / L) : 1.f;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (pc.t0 == 0 ? 1 : 0);
       float* part = p.part_o + (slot * kRows + i) * kD + hf * 64;
       unsigned char* dst = p.out + 2 * (pc.b * p.o_batch + node * p.o_token + head * p.o_head + hf * 64);

@@ -556,10 +556,16 @@ lyc_status lyc_cache_read(const lyc_layer_cache* cache, const lyc_read_args* arg
  * t >= t_len[b] are padding: not read, outputs as they were.  1 <= T <= 256.
  * Scores, sums and the softmax are fp32; the probabilities are rounded to the
  * 16-bit type of the second product: bf16, or over an E4M3 cache fp16 together
- * with V's scale.  There what is below 2^-30 of a query's largest probability *
- * scale is lost, and a query's elements below 2^-17 of its largest are rounded
- * to 2^-24 of that.  (There the scales of rows that are not seen may choose
- * between two roundings.)  The result of a call does not depend on
+ * with V's scale.  There a probability * scale is off by at most 2^-11 of itself
+ * and 2^-30 of the query's largest; the softmax's sum has the probabilities in
+ * fp32, and a row drops out of it only where its probability * scale is below
+ * 2^-110 of the largest, as a row of zeros (scale 2^-100) may beside rows of V
+ * above 10^5.  A query's elements below 2^-17 of its largest are rounded to 2^-24
+ * of that.  Of scale bytes that the writer never makes, V's below 27 count as 27,
+ * and K's 0 may count as 1.
+ * (The scales of rows that are not seen may choose between two roundings.)
+ * Sums over rows are divided at the end: over a BF16 cache, 2^8 n max|v| has to be
+ * within fp32's range.  The result of a call does not depend on
  * the order in which the GPU runs its blocks.
  *   q, out  [batch][T][num_q_heads][head_dim] bf16, num_q_heads a multiple of
  *           num_kv_heads

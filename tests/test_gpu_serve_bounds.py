@@ -124,3 +124,39 @@ def test_e4m3_probabilities_are_fp16(lyc, T, hq, hkv, d, page, n):
         b = x.view(torch.uint8)
         b &= 0x7F
     strict(lyc, cache, q * 0.125, lens, cnt, None, what="one sign")
+
+
+# ------------------------------------------------------------------ sums
+
+
+@pytest.mark.parametrize("T,hq", [(1, 4), (3, 8), (40, 2), (70, 2)])
+def test_rows_of_the_smallest_scales(lyc, T, hq):
+    """Rows that are counted but were never written (zero codes, scale byte 0) are
+    rows of zeros of their own tiles and blocks, beside written ones: they count in
+    the sum."""
+    d, rows = 128, 20000
+    cache = fill(lyc, 2, 1, d, rows, 0, True, seed=40)
+    for x in cache.tensors[:4]:
+        b = x.view(torch.uint8)
+        b[0, :, :15000] = 0
+        b[1, :, 400:] = 0
+    strict(lyc, cache, randn(1, 2, T, hq, d), [rows, rows], None, None, what="unwritten")
+
+
+@pytest.mark.parametrize("step", [4, 8])
+@pytest.mark.parametrize("T", [1, 40, 70])
+def test_long_runs_of_zero_values(lyc, T, step):
+    """A quarter of a million V rows of zeros (scale 2^-100) in one block, their logits
+    as far above the first ones as the running maximum does not move for: the sum
+    stays finite, and the one row of ones has its share."""
+    rows = 1 << 18
+    one = lyc.KvCache.empty(1, 1, 128, rows=rows + T)
+    plain_scales(one)
+    k, v, _, vs, _ = one.tensors
+    vs.view(torch.uint8).fill_(27)
+    k[0, 0, :, 0] = e4m3(-16.0)
+    k[0, 0, 4096:, 0] = e4m3(-16.0 + step)
+    k[0, 0, rows - 1, 0] = e4m3(0.0)
+    v[0, 0, rows - 1] = e4m3(256.0)
+    vs.view(torch.uint8)[0, 0, rows - 1] = 119
+    check_shared(lyc, one, one_hot(T), rows + T, None, "zeros")
