@@ -160,3 +160,60 @@ def test_long_runs_of_zero_values(lyc, T, step):
     v[0, 0, rows - 1] = e4m3(256.0)
     vs.view(torch.uint8)[0, 0, rows - 1] = 119
     check_shared(lyc, one, one_hot(T), rows + T, None, "zeros")
+
+
+# ------------------------------------------------------------------ states merged within a block
+
+
+def whole_groups(n, hkv, blocks, sms=148, tile=128):
+    """By CTA, the tiles of each group that its run holds whole (the runs are equal
+    shares of all tiles)."""
+    spans, total = [], 0
+    for nb in n:
+        for _ in range(hkv * blocks):
+            t = -(-nb // tile)
+            spans.append((total, total + t))
+            total += t
+    grid = min(sms, total)
+    share, more = divmod(total, grid)
+    runs = [c * share + min(c, more) for c in range(grid + 1)]
+    return [[b - a for a, b in spans if runs[c] <= a and b <= runs[c + 1]] for c in range(grid)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,hq", [(12, 32), (16, 32), (40, 8)])
+def test_long_whole_groups_of_few_rows(lyc, e4m3, T, hq):
+    """Blocks of 33 to 64 query rows whose whole group, 16 tiles or more, is one CTA's:
+    its query rows lie in the lanes twice, and the copies are merged there.  Short
+    groups, with one copy, and cut ones come between.  A drafted V row holds a NaN (an
+    infinity beside it, over bf16 rows) that some nodes see."""
+    B, hkv, d, page, pool = 40, 8, 128, 16, 600
+    rng = np.random.default_rng(T + e4m3)
+    n = [int(rng.integers(2048, 4000)) if b % 3 else int(rng.integers(T + 20, 1900)) for b in range(B)]
+    n[4] = n[5] = 2048
+    groups = whole_groups(n, hkv, 1, torch.cuda.get_device_properties(0).multi_processor_count)
+    merged = [[t >= 16 for t in g] for g in groups]
+    assert sum(map(sum, merged)) > 50 and any(any(m) and not all(m) for m in merged)
+    proto = fill(lyc, 1, hkv, d, (pool + 5 * B) * page, page, e4m3, seed=T)
+    k, v, ks, vs, _ = proto.tensors
+    table = rng.integers(0, pool, (B, 4000 // page + 1))
+    for b in range(B):  # the drafted rows' pages are the element's own
+        last = (n[b] - 1) // page
+        for i in range(5):
+            if last - i >= 0:
+                table[b, last - i] = pool + 5 * b + i
+    cache = lyc.KvCache(k, v, ks, vs, block_table=i32(table.tolist()))
+    for b in range(0, B, 2):
+        row = n[b] - T + 3
+        at = (int(table[b, row // page]), row % page)
+        if e4m3:
+            vs.view(torch.uint8)[at[0], at[1], b % hkv] = 255
+        else:
+            v[at[0], at[1], b % hkv, 5] = math.nan
+            v[at[0], at[1], b % hkv, 70] = math.inf
+    mask = random_tree(rng, B, T)
+    q = randn(T, B, T, hq, d)
+    out = strict(lyc, cache, q, n, None, mask, what="whole groups")
+    assert torch.isnan(out.float()).any() and torch.isfinite(out.float()).any()
+    again, _ = run_tree(lyc, cache, q, n, None, mask)
+    assert torch.equal(again.view(torch.int16), out.view(torch.int16))
