@@ -217,3 +217,46 @@ def test_long_whole_groups_of_few_rows(lyc, e4m3, T, hq):
     assert torch.isnan(out.float()).any() and torch.isfinite(out.float()).any()
     again, _ = run_tree(lyc, cache, q, n, None, mask)
     assert torch.equal(again.view(torch.int16), out.view(torch.int16))
+
+
+# ------------------------------------------------------------------ bytes of the cache
+
+
+@pytest.mark.parametrize("page", [0, 7, 16, 64])
+def test_append_writes_its_rows_and_no_other_byte(lyc, page):
+    """Codes and scales of K and of V against the definition by search, and every other
+    byte of the four tensors as it was, around rows written at ragged lengths; then
+    the same where elements and pages are refused."""
+    B, T, hkv, d, cap = 4, 9, 3, 128, 130
+    rng = np.random.default_rng(page)
+    cache = fill(lyc, B, hkv, d, cap, page, True, seed=50 + page)
+    tensors = [x.view(torch.uint8) for x in cache.tensors[:4]]
+    bt = cache.tensors[4]
+    for refuse in (False, True):
+        before = [x.clone() for x in tensors]
+        cnt = [T, 0, 4, 1]
+        n = [cap, 77, 4, 65]
+        bad = set()
+        if refuse:
+            n[0] = 3  # fewer rows than tokens
+            bad.add(0)
+            if page:
+                bt[3, 64 // page] = 10**6
+                bad.add(3)
+        k, v = randn(60 + refuse, B, T, hkv, d), randn(61 + refuse, B, T, hkv, d, scale=1e-3)
+        st = status_word()
+        lyc.cache_append(cache, i32(n), k, v, t_len=i32(cnt), status=st)
+        assert (int(st) != 0) == refuse
+        want = [x.clone() for x in before]
+        for b in range(B):
+            if b in bad:
+                continue
+            for t in range(cnt[b]):
+                row = n[b] - cnt[b] + t
+                for i, x in ((0, k), (1, v)):
+                    code, byte = SS.e4m3_row(x[b, t].cpu())
+                    at = (b, slice(None), row) if bt is None else (int(bt[b, row // page]), row % page)
+                    want[i][at] = code.to(torch.uint8).cuda()
+                    want[2 + i][at] = byte.to(torch.uint8).cuda()
+        for name, x, w in zip(("k", "v", "k_scale", "v_scale"), tensors, want):
+            assert torch.equal(x, w), name
