@@ -1,6 +1,6 @@
 // serve_api.cu -- host side of the serving operators (include/lyc.h, "Serving
 // operators"): argument checks and launches.  No state but the per-thread
-// message of lyc_operator_error; nothing here allocates or throws.
+// message and code of the last failure; nothing here allocates or throws.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdarg.h>
@@ -17,13 +17,14 @@ using namespace lyc;
 namespace {
 
 thread_local char g_error[256];
+thread_local lyc_status g_status = LYC_OK;
 
 lyc_status refuse(lyc_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_error, sizeof g_error, fmt, ap);
   va_end(ap);
-  return s;
+  return g_status = s;
 }
 
 lyc_status launched(cudaError_t e, const char* what) {
@@ -210,6 +211,7 @@ lyc_status check_tree(const lyc_layer_cache* c, int T, int Hq) {
 extern "C" {
 
 const char* lyc_operator_error(void) { return g_error; }
+lyc_status lyc_operator_status(void) { return g_status; }
 
 lyc_status lyc_qk_norm_rope(const lyc_rope_args* a, void* stream) {
   if (!a) return refuse(LYC_ERR_INVALID_ARG, "NULL arguments");

@@ -67,7 +67,7 @@ EXPORTED = ["lyc_create", "lyc_decode_step", "lyc_decode_step_host", "lyc_decode
             "lyc_kernel_times", "lyc_set_timeline", "lyc_status_string", "lyc_last_error",
             "lyc_destroy", "lyc_sparse_attention_noalloc", "lyc_set_selection", "lyc_cache_correction",
             "lyc_qk_norm_rope", "lyc_cache_append", "lyc_cache_read", "lyc_tree_workspace_bytes",
-            "lyc_tree_attention", "lyc_operator_error"]
+            "lyc_tree_attention", "lyc_operator_error", "lyc_operator_status"]
 
 
 class lyc_config(ctypes.Structure):
@@ -329,6 +329,11 @@ def lyc_tree_attention(cache: lyc_layer_cache, args: lyc_tree_args, stream) -> i
 
 def lyc_operator_error() -> str:
     return load().lyc_operator_error().decode()
+
+
+def lyc_operator_status() -> int:
+    """The code of this thread's last failing serving operator, LYC_OK if none did."""
+    return load().lyc_operator_status()
 
 
 # ------------------------------------------------------------ torch wrapper
@@ -809,6 +814,6 @@ def tree_workspace_bytes(cache, T: int, num_q_heads: int) -> int:
     if need is None:
         need = lyc_tree_workspace_bytes(cache.desc, T, num_q_heads)
         if need == 0:
-            raise LycError(LYC_ERR_INVALID_ARG, "lyc_tree_workspace_bytes", lyc_operator_error())
+            raise LycError(lyc_operator_status(), "lyc_tree_workspace_bytes", lyc_operator_error())
         cache._workspace[(T, num_q_heads)] = need
     return need

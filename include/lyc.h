@@ -590,6 +590,8 @@ lyc_status lyc_tree_attention(const lyc_layer_cache* cache, const lyc_tree_args*
 
 /* Why this thread's last failing serving operator failed ("" if none did). */
 const char* lyc_operator_error(void);
+/* ... and with which code (LYC_OK if none did): lyc_tree_workspace_bytes has no other way to say it. */
+lyc_status lyc_operator_status(void);
 
 const char* lyc_status_string(lyc_status s);
 const char* lyc_last_error(const lyc_ctx* ctx);
