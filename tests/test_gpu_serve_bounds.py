@@ -260,3 +260,33 @@ def test_append_writes_its_rows_and_no_other_byte(lyc, page):
                     want[2 + i][at] = byte.to(torch.uint8).cuda()
         for name, x, w in zip(("k", "v", "k_scale", "v_scale"), tensors, want):
             assert torch.equal(x, w), name
+
+
+# ------------------------------------------------------------------ errors
+
+
+def test_a_refused_device_leaves_no_error_behind(lyc):
+    """A device that is not there is refused with its code, the current device stays,
+    and the program's next CUDA calls do not meet the error."""
+    cache = fill(lyc, 1, 1, 64, 40, 0, False, seed=1)
+    q = randn(2, 1, 2, 2, 64)
+    out, _ = run_tree(lyc, cache, q, [40])
+    a = lyc.lyc_layer_cache.from_buffer_copy(cache.desc)
+    a.device = torch.cuda.device_count() + 7
+    assert lyc.lyc_tree_workspace_bytes(a, 2, 2) == 0 and lyc.lyc_operator_status() == lyc.LYC_ERR_CUDA
+    n, ko = i32([40]), torch.zeros((1, 1, 4, 64), dtype=BF, device="cuda")
+    args = lyc.lyc_read_args(ko.data_ptr(), ko.data_ptr(), 256, 256, 64, n.data_ptr(), None, 0, 4, 1, lyc.LYC_BF16, None)
+    assert lyc.lyc_cache_read(a, args, None) == lyc.LYC_ERR_CUDA
+    assert torch.cuda.current_device() == 0
+    again, _ = run_tree(lyc, cache, q, [40])
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+    # an entry point that asks for the last error after its launch
+    qs, k = randn(3, 1, 2, 64), randn(4, 1, 1, 1, 40, 64)
+    kv = lyc.lyc_kv_cache(k.data_ptr(), k.data_ptr(), 40, 0, *k.stride()[1:4])
+    S = torch.arange(8, device="cuda", dtype=torch.int32).expand(1, 2, 8).contiguous()
+    o = torch.empty((1, 2, 64), device="cuda")
+    assert lyc.lyc_cache_read(a, args, None) == lyc.LYC_ERR_CUDA
+    assert lyc.lyc_sparse_attention_noalloc(qs.data_ptr(), kv, 1, 2, 1, 64, S.data_ptr(), 8, o.data_ptr(), None,
+                                            torch.cuda.current_stream().cuda_stream) == lyc.LYC_OK
+    torch.cuda.synchronize()
