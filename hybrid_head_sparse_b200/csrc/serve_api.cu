@@ -47,6 +47,8 @@ struct OnDevice {
   }
 };
 
+// Words that the kernels read one at a time (lengths, positions, masks, the status).
+bool off_word(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1u)) != 0; }
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 constexpr int64_t kMaxRows = 1ll << 30;
@@ -73,6 +75,7 @@ lyc_status check_cache(const lyc_layer_cache* c, bool writes) {
   if (!f8 && (c->k_scale || c->v_scale)) return refuse(LYC_ERR_INVALID_ARG, "a bf16 cache has no scales");
   const int per16 = f8 ? 16 : 8;
   int64_t cap = c->rows;
+  if (off_word(c->block_table, 4)) return refuse(LYC_ERR_INVALID_ARG, "block_table must be 4-byte aligned");
   if (c->block_table) {
     if (c->page_rows < 1 || c->max_blocks < 1 || c->num_pages < 1 || c->num_pages > 0x7fffffffll)
       return refuse(LYC_ERR_INVALID_ARG, "paged cache needs page_rows, max_blocks and num_pages >= 1");
@@ -225,6 +228,8 @@ lyc_status lyc_qk_norm_rope(const lyc_rope_args* a, void* stream) {
   const lyc_status st = check_rotation(a->rot_dim, a->head_dim, a->inv_freq, a->eps);
   if (st != LYC_OK) return st;
   if (a->rot_dim > 0 && !a->pos) return refuse(LYC_ERR_INVALID_ARG, "a rotation needs pos");
+  if (a->rot_dim > 0 && (off_word(a->pos, 4) || off_word(a->inv_freq, 4)))
+    return refuse(LYC_ERR_INVALID_ARG, "pos and inv_freq must be 4-byte aligned");
   if (a->q) {
     if (!a->q_out || misaligned(a->q) || misaligned(a->q_out) || misaligned(a->q_weight))
       return refuse(LYC_ERR_INVALID_ARG, "q, q_out and q_weight must be 16-byte aligned");
@@ -287,6 +292,8 @@ lyc_status lyc_cache_append(const lyc_layer_cache* c, const lyc_append_args* a, 
   if (st != LYC_OK) return st;
   if (misaligned(a->k) || misaligned(a->v) || misaligned(a->k_weight))
     return refuse(LYC_ERR_INVALID_ARG, "k, v and k_weight must be 16-byte aligned");
+  if (off_word(a->n, 4) || off_word(a->t_len, 4) || off_word(a->pos, 4) || off_word(a->inv_freq, 4) || off_word(a->status, 4))
+    return refuse(LYC_ERR_INVALID_ARG, "n, t_len, pos, inv_freq and status must be 4-byte aligned");
   if (stride_bad(a->k_batch, c->batch, 8) || stride_bad(a->k_token, a->T, 8) ||
       stride_bad(a->k_head, c->num_kv_heads, 8) || stride_bad(a->v_batch, c->batch, 8) ||
       stride_bad(a->v_token, a->T, 8) || stride_bad(a->v_head, c->num_kv_heads, 8))
@@ -355,6 +362,8 @@ lyc_status lyc_cache_read(const lyc_layer_cache* c, const lyc_read_args* a, void
   if (a->num_heads < 1 || a->num_heads > kMaxHeads || a->num_heads % c->num_kv_heads != 0 ||
       (!a->sets && a->num_heads != c->num_kv_heads))
     return refuse(LYC_ERR_INVALID_ARG, "num_heads %d does not fit num_kv_heads %d", a->num_heads, c->num_kv_heads);
+  if (off_word(a->n, 4) || off_word(a->sets, 4) || off_word(a->status, 4))
+    return refuse(LYC_ERR_INVALID_ARG, "n, sets and status must be 4-byte aligned");
   if (a->sets && a->first != 0) return refuse(LYC_ERR_INVALID_ARG, "sets and first do not go together");
   const int per16 = a->dtype == LYC_BF16 ? 8 : 4;
   if (misaligned(a->k_out) || misaligned(a->v_out) || stride_bad(a->o_batch, c->batch, per16) ||
@@ -400,6 +409,8 @@ lyc_status lyc_tree_attention(const lyc_layer_cache* c, const lyc_tree_args* a, 
   if (st != LYC_OK) return st;
   if (!a->q || !a->out || !a->n || misaligned(a->q) || misaligned(a->out))
     return refuse(LYC_ERR_INVALID_ARG, "q and out must be 16-byte aligned device pointers, n not NULL");
+  if (off_word(a->n, 4) || off_word(a->t_len, 4) || off_word(a->mask, 8) || off_word(a->status, 4))
+    return refuse(LYC_ERR_INVALID_ARG, "n, t_len and status must be 4-byte aligned, mask 8");
   if (!(a->scale > 0.f) || isinf(a->scale)) return refuse(LYC_ERR_INVALID_ARG, "scale must be a finite number > 0");
   if (stride_bad(a->q_batch, c->batch, 8) || stride_bad(a->q_token, a->T, 8) || stride_bad(a->q_head, a->num_q_heads, 8) ||
       stride_bad(a->o_batch, c->batch, 8) || stride_bad(a->o_token, a->T, 8) || stride_bad(a->o_head, a->num_q_heads, 8))

@@ -411,6 +411,7 @@ lyc_status lyc_sparse_attention_noalloc(const void* q, const lyc_kv_cache* kv, i
  * are in elements of their tensor; the head_dim elements of a row are
  * contiguous, and every row starts on a 16-byte boundary (pointers 16-byte
  * aligned, strides multiples of 16 bytes; LYC_ERR_INVALID_ARG otherwise).
+ * Other arrays are aligned as their elements.
  * Strides are >= 0.  Where a dimension has one entry its stride is not used.
  *
  * Errors found on the host are returned at once, nothing is enqueued, and
