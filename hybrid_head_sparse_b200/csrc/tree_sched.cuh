@@ -94,7 +94,7 @@ struct TreeSched : TreeLens<TR, ROWS> {
   uint32_t total;
   uint32_t grid;         // CTAs that have tiles
   uint32_t share, more;  // the first `more` CTAs have share + 1 tiles, the others share
-  uint32_t per, nt1;     // groups of one length (one element): CTAs and tiles of each; per 0: as above
+  uint32_t per, nt1;     // one element's groups: CTAs and tiles of each; per 0: as above
 
   __device__ __forceinline__ explicit TreeSched(const TreeParams& prm) : TreeLens<TR, ROWS>(prm, 0, 0u) {
     total = __shfl_sync(0xffffffffu, this->upto, 31);
@@ -108,15 +108,21 @@ struct TreeSched : TreeLens<TR, ROWS> {
     per = 0;
     nt1 = 1;
     if (prm.B == 1) {
-      // as many CTAs for each group, so that no run spans two groups (a second
-      // start and merge in one CTA costs more than the few CTAs left over: one
-      // token at 4097 rows, 144 CTAs against 148)
+      // as many CTAs for each group, so that no run spans two groups, where that
+      // leaves at most a sixteenth of them over.  In us against equal runs, one
+      // token over 4 h / h heads of 128:
+      //   few left over: h 8, 4097 rows bf16 10.0, 12.2; 65536 bf16 47.6, 48.4, e4m3 36.2, 39.0
+      //   many: h 40, 65536 rows e4m3 151, 126; h 64 bf16 332, 320, e4m3 222, 192
+      // and 160 nodes over 32768 rows, 64 / 8 heads (80 groups) bf16 350, 225, e4m3 485, 322
       const TreeElem e = this->elem(0);
       const uint32_t groups = static_cast<uint32_t>(prm.Hkv * this->blocks(e));
       nt1 = static_cast<uint32_t>((e.n + TR - 1) / TR);
       if (groups > 0 && grid >= groups) {
-        per = min(grid / groups, nt1);
-        grid = groups * per;
+        const uint32_t each = min(grid / groups, nt1);
+        if ((grid - groups * each) * 16u <= grid) {
+          per = each;
+          grid = groups * each;
+        }
       }
     }
     share = total / grid;

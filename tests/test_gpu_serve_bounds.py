@@ -219,6 +219,20 @@ def test_long_whole_groups_of_few_rows(lyc, e4m3, T, hq):
     assert torch.equal(again.view(torch.int16), out.view(torch.int16))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("T,hq,hkv,d,n", [(1, 40, 40, 64, 3000), (1, 100, 50, 128, 5000), (2, 96, 96, 64, 900),
+                                          (160, 64, 8, 128, 1200), (128, 64, 8, 128, 700), (3, 149, 149, 64, 600)])
+def test_one_element_of_many_groups(lyc, e4m3, T, hq, hkv, d, n):
+    """One element whose groups do not divide the blocks evenly: runs cut across
+    groups, or whole blocks for each."""
+    cache = fill(lyc, 1, hkv, d, n, 0, e4m3, seed=hkv)
+    q = randn(T, 1, T, hq, d)
+    mask = random_tree(np.random.default_rng(T), 1, T)
+    out = strict(lyc, cache, q, [n], None, mask, what="one element")
+    again, _ = run_tree(lyc, cache, q, [n], None, mask)
+    assert torch.equal(out, again)
+
+
 # ------------------------------------------------------------------ bytes of the cache
 
 
