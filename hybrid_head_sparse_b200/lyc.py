@@ -535,6 +535,7 @@ _ROPE_ARGS = struct.Struct("@4P8q4Pq5if2i")
 _APPEND_ARGS = struct.Struct("@4P12q6P4ifP")
 _READ_ARGS = struct.Struct("@2P3q2Pq3iP")
 _TREE_ARGS = struct.Struct("@2P6q3P2ifPQP")
+_NO_FIT = (struct.error, OverflowError)
 
 
 def _operators():
@@ -695,9 +696,12 @@ def qk_norm_rope(q, k, pos, inv_freq, q_out, k_out, q_weight=None, k_weight=None
             _refuse(where, "a rotation needs pos")
         fp = _packed(where, "inv_freq", inv_freq, torch.float32, (half,), index)
         pp = _packed(where, "pos", pos, torch.int32, (rows,), index)
-    args = _ROPE_ARGS.pack(qp, kp, qo, ko, sq[0], sq[1], sk[0], sk[1], sqo[0], sqo[1], sko[0], sko[1], pp, fp, qw, kw,
-                           rows, hq, hk, d, rot, 1 if interleaved else 0, eps,
-                           LYC_BF16 if dtype is torch.bfloat16 else LYC_FP32, index)
+    try:
+        args = _ROPE_ARGS.pack(qp, kp, qo, ko, sq[0], sq[1], sk[0], sk[1], sqo[0], sqo[1], sko[0], sko[1], pp, fp, qw, kw,
+                               rows, hq, hk, d, rot, 1 if interleaved else 0, eps,
+                               LYC_BF16 if dtype is torch.bfloat16 else LYC_FP32, index)
+    except _NO_FIT as e:
+        _refuse(where, f"a number does not fit its argument: {e}")
     rc = _operators().lyc_qk_norm_rope(args, _stream_on(index, stream))
     if rc:
         _operator_check(rc, "lyc_qk_norm_rope")
@@ -736,11 +740,14 @@ def cache_append(cache, n, k, v, t_len=None, q=None, q_out=None, pos=None, inv_f
         half = inv_freq.numel()
         rot = 2 * half
         fp = _packed(where, "inv_freq", inv_freq, torch.float32, (half,), index)
-    args = _APPEND_ARGS.pack(
-        kp, vp, qp, qo, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], sq[0], sq[1], sq[2], sqo[0], sqo[1], sqo[2],
-        _packed(where, "n", n, i32, (B,), index), _packed(where, "t_len", t_len, i32, (B,), index),
-        _packed(where, "pos", pos, i32, (B, T), index), fp, qw, _packed(where, "k_weight", k_weight, bf16, (d,), index),
-        T, hq, rot, 1 if interleaved else 0, eps, _status_ptr(where, status, index))
+    try:
+        args = _APPEND_ARGS.pack(
+            kp, vp, qp, qo, sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], sq[0], sq[1], sq[2], sqo[0], sqo[1], sqo[2],
+            _packed(where, "n", n, i32, (B,), index), _packed(where, "t_len", t_len, i32, (B,), index),
+            _packed(where, "pos", pos, i32, (B, T), index), fp, qw, _packed(where, "k_weight", k_weight, bf16, (d,), index),
+            T, hq, rot, 1 if interleaved else 0, eps, _status_ptr(where, status, index))
+    except _NO_FIT as e:
+        _refuse(where, f"a number does not fit its argument: {e}")
     rc = _operators().lyc_cache_append(cache._desc_ref, args, _stream_on(index, stream))
     if rc:
         _operator_check(rc, "lyc_cache_append")
@@ -761,9 +768,12 @@ def cache_read(cache, n, k_out, v_out, sets=None, first=0, status=None, stream=N
     vp, sv = _rows_in(where, "v_out", v_out, dtype, shape, index)
     if so != sv:
         _refuse(where, "k_out and v_out must have the same strides")
-    args = _READ_ARGS.pack(kp, vp, so[0], so[1], so[2], _packed(where, "n", n, torch.int32, (B,), index),
-                           _packed(where, "sets", sets, torch.int32, (B, H, m), index), first, m, H,
-                           LYC_BF16 if dtype is torch.bfloat16 else LYC_FP32, _status_ptr(where, status, index))
+    try:
+        args = _READ_ARGS.pack(kp, vp, so[0], so[1], so[2], _packed(where, "n", n, torch.int32, (B,), index),
+                               _packed(where, "sets", sets, torch.int32, (B, H, m), index), first, m, H,
+                               LYC_BF16 if dtype is torch.bfloat16 else LYC_FP32, _status_ptr(where, status, index))
+    except _NO_FIT as e:
+        _refuse(where, f"a number does not fit its argument: {e}")
     rc = _operators().lyc_cache_read(cache._desc_ref, args, _stream_on(index, stream))
     if rc:
         _operator_check(rc, "lyc_cache_read")
@@ -799,10 +809,13 @@ def tree_attention(q, cache, n, out, mask=None, t_len=None, scale=None, workspac
                 workspace = q.new_empty((need + 1) // 2)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         _refuse(where, f"workspace must be contiguous, on cuda:{index}")
-    args = _TREE_ARGS.pack(qp, op, sq[0], sq[1], sq[2], so[0], so[1], so[2], _packed(where, "n", n, i32, (B,), index),
-                           _packed(where, "t_len", t_len, i32, (B,), index), mp, T, hq,
-                           cache.d**-0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes,
-                           _status_ptr(where, status, index))
+    try:
+        args = _TREE_ARGS.pack(qp, op, sq[0], sq[1], sq[2], so[0], so[1], so[2], _packed(where, "n", n, i32, (B,), index),
+                               _packed(where, "t_len", t_len, i32, (B,), index), mp, T, hq,
+                               cache.d**-0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes,
+                               _status_ptr(where, status, index))
+    except _NO_FIT as e:
+        _refuse(where, f"a number does not fit its argument: {e}")
     rc = _operators().lyc_tree_attention(cache._desc_ref, args, _stream_on(index, stream))
     if rc:
         _operator_check(rc, "lyc_tree_attention")

@@ -304,3 +304,22 @@ def test_a_refused_device_leaves_no_error_behind(lyc):
     assert lyc.lyc_sparse_attention_noalloc(qs.data_ptr(), kv, 1, 2, 1, 64, S.data_ptr(), 8, o.data_ptr(), None,
                                             torch.cuda.current_stream().cuda_stream) == lyc.LYC_OK
     torch.cuda.synchronize()
+
+
+def test_numbers_that_do_not_fit_are_refused(lyc):
+    """An eps or a scale past fp32, a first row past 64 bits, what is no number: refused
+    as other wrong arguments are."""
+    cache = fill(lyc, 1, 1, 64, 40, 0, True, seed=1)
+    q, k, n, ko = randn(2, 1, 2, 2, 64), randn(3, 1, 2, 1, 64), i32([40]), torch.zeros((1, 1, 4, 64), dtype=BF, device="cuda")
+    out, v = torch.zeros_like(q), ko.clone()
+    bad = [lambda: lyc.qk_norm_rope(q[0], None, None, None, out[0], None, eps=1e39),
+           lambda: lyc.cache_append(cache, n, k, k, eps=1e39),
+           lambda: lyc.cache_append(cache, n, k, k, eps="small"),
+           lambda: lyc.cache_read(cache, n, ko, v, first=1 << 64),
+           lambda: lyc.cache_read(cache, n, ko, v, first=0.5),
+           lambda: lyc.tree_attention(q, cache, n, out, scale=1e39)]
+    for i, call in enumerate(bad):
+        with pytest.raises(lyc.LycError) as e:
+            call()
+        assert e.value.code == lyc.LYC_ERR_INVALID_ARG, i
+    assert not out.any() and not ko.any()
