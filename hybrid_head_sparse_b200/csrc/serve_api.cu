@@ -159,7 +159,7 @@ int sm_count(int device) {
 //   bf16, 16 rows   mma.sync  86   32  10   23  24
 //   bf16, 32 rows   mma.sync  99   43  14   35  42   tcgen05  90  33  14  29  33
 //   e4m3, 32 rows   mma.sync 122   44  15   32  36   tcgen05 106  48  20  41  49
-//   e4m3, 36 rows   mma.sync 214   62  16   51  57   tcgen05 108  50  21  43  50
+//   e4m3, 36 rows   mma.sync 214   62  16   51  57   tcgen05 111  50  21  43  50
 // (mma.sync has blocks of 16 or 32 rows, so more read the cache again; the capacity
 // that the host knows says little of the lengths.)
 constexpr int mma_most_rows(int cache_type) { return cache_type == LYC_CACHE_BF16 ? 16 : 32; }

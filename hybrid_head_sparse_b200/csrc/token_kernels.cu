@@ -108,8 +108,9 @@ __device__ __forceinline__ int scale_byte(uint32_t max_bits) {
 // registers, and fp32 runs two operations an instruction: the first form (a
 // lane with 16 adjacent bytes, partners by shuffle, turns from shared memory)
 // was bound by instructions, 250 a row against about 60.  8192 tokens of 32/8
-// heads of 128 bf16: 36.5 us, 4.6 TB/s, 0.70 of the copy rate, and still six
-// issue slots of ten; written into an e4m3 cache, with the values, 43.5 us.  (Two
+// heads of 128 bf16: 36.8 us, 4.6 TB/s, 0.70 of the copy rate, and still six
+// issue slots of ten; written into an e4m3 cache, with the values, 43.7 us (0.64),
+// into a bf16 cache 43 (0.71).  (Two
 // rounds of heads in flight instead of one: 35.8 and 44.3.)
 //
 // The token's angles are taken once, in 64 bits: the turn pos * inv_freq /
@@ -313,8 +314,9 @@ __global__ void __launch_bounds__(512) token_kernel(const __grid_constant__ Toke
 // ---------------------------------------------------------------- read back
 // Each thread takes 16 bytes of K and of V of one row; a block takes
 // kReadThreads / LPR entries of one (element, head).  32768 rows of 8 heads of
-// 128, e4m3 to bf16: 37.3 us, 5.4 TB/s, 0.82 of the copy rate.  (Two or four rows a
-// thread, asked for together: 43.)
+// 128, e4m3 to bf16: 37.7 us, 5.4 TB/s, 0.82 of the copy rate; e4m3 to fp32 74 us
+// (0.69); a bf16 cache to bf16 40.8 us (1.00).  (Two or four rows a thread, asked for
+// together: 43.)
 constexpr int kReadThreads = 256;
 
 __device__ __forceinline__ float e8m0(int byte) {

@@ -22,13 +22,15 @@
 // free in a sum over the head's dimensions, so K's codes are read 16 bytes at
 // a time in an order that needs no shuffling and Q is laid out to match.  A
 // query row is scaled by a power of two to below 2 before it becomes f16
-// (exact for elements down to 2^-14 of the row's largest).  V's scales 2^e_j
+// (exact for elements down to 2^-17 of the row's largest).  V's scales 2^e_j
 // go into the exponent: p'_j = 2^(z_j + e_j - m'), m' the running maximum of
 // z_j + e_j, so p' stays in f16's range whatever the scales are, and the sum
-// takes p'_j 2^-e_j (kSumUnitE4m3).  One token over 131072 such rows: 61 us, 0.67 of the floor (8192 x 4:
-// 24, 0.43; head_dim 64: 48), bound by instructions and their chains: codes
-// converted by bit moves took 74, 16 rows at a time 66 (32 at a time cost a cache
-// of 300 rows 1 us of 18), 12 warps of half the chunk no less.
+// takes p'_j 2^-e_j (kSumUnitE4m3).  One token over 131072 such rows: 63 us, 0.66 of
+// the floor (8192 x 4: 24, 0.42; head_dim 64: 49, 0.42), bound by chains of
+// instructions (the issue slots are busy for 0.4 of the time): codes converted by bit
+// moves took 74, 16 rows at a time 66 (32 at a time cost a cache of 300 rows 1 us of
+// 18), 12 warps of half the chunk no less.  32 query rows: 122 us, 0.34; the 255
+// registers a thread do not hold the queries and the output, and some spill.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

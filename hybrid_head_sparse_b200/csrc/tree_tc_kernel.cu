@@ -40,13 +40,14 @@
 // the rows of coming tiles and their scales; eight producer warps copy the codes
 // in, convert them (two instructions for two codes) and store them.
 //
-// Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 92 to
-// 98 us, 5.5 to 5.8 TB/s, 0.84 to 0.89 of the copy rate: HBM, and the
-// exponentials (1024 cycles of a tile's 2600).  4 x 16 nodes over up to 65536
-// e4m3 rows each: 165 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 114 to 137.
-// There a tile takes 3200 cycles against the 1300 of its bytes: 1000 of the tensor
-// cores, 1800 of shared memory, and the softmax warps' chain of latencies, which
-// twenty warps on an SM stretch to 2500.  Slower were: bf16 tiles, codes converted by
+// Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 96 to
+// 101 us by the box, 5.3 to 5.6 TB/s, 0.81 to 0.85 of the copy rate: HBM, and the
+// exponentials (1024 cycles a tile at 16 a cycle).  4 x 16 nodes over up to 65536
+// e4m3 rows each: 165 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 114 to 135.
+// There a tile's share is 2.0 us, its bytes' 0.75; counted, it needs 1000 cycles of
+// the tensor cores and 1800 of shared memory (128 bytes a cycle), and neither is busy
+// for more than a third of the time (half of the issue slots are): what bounds it is
+// the softmax warps' chain of latencies among twenty warps.  Slower were: bf16 tiles, codes converted by
 // bit moves (175); each row's own scale in the softmax, K's codes as an e4m3 operand
 // (212); codes brought by TMA (205); four or sixteen producers (190, 203); a fourth
 // finder (200: the schedulers' warps are no longer the same); one pass over the
@@ -394,9 +395,9 @@ struct RowInfo {
 
 // A finder warp finds the rows of every third tile of the run, lane j rows j + 32 k:
 // pages are asked for a turn ahead, and a tile's scales arrive while the next
-// one's rows are found.  A turn is a chain of some 4000 cycles, so one warp was
-// what a tile took.  (In the producers, a row a lane, it cost them 1200 cycles a
-// tile: their waits for shared memory are also waits for the loads that share a
+// one's rows are found.  A turn is a chain of dependent loads that is longer than a
+// tile, so one warp was what a tile took.  (In the producers, a row a lane, it held
+// them up: their waits for shared memory are also waits for the loads that share a
 // counter.)
 template <class C>
 __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* smem) {
@@ -506,8 +507,8 @@ __device__ __forceinline__ void tc_rows(const TreeTcParams& P, unsigned char* sm
 // of a tile, eight lanes a row.  A lane copies its 16 codes of a unit to shared
 // memory kRawRing groups ahead and converts what it copied itself, so a warp waits for
 // nobody's copies but its own.  (With the codes kept in registers instead, the
-// loops had to be unrolled over them and, with the softmax's, outgrew the SM's
-// instruction cache: 7600 cycles a tile, 40% of the instruction fetches missing.)
+// loops had to be unrolled over them and, with the softmax's, were larger than the
+// SM's instruction cache: more than twice the time.)
 template <class C>
 __device__ __forceinline__ void tc_produce(const TreeTcParams& P, unsigned char* smem) {
   const TreeParams& p = P.t;
@@ -540,7 +541,7 @@ __device__ __forceinline__ void tc_produce(const TreeTcParams& P, unsigned char*
       const RowInfo* rows = info + (t % kInfoRing) * kRows + g * (kRows / kGroups);
       unsigned char* dst = tiles + stage * C::TILEB + g * (kRows / kGroups) * 128;
       // (all loads before the first store: the compiler cannot tell them apart, and
-      // one unit after another ran at 200 cycles a unit)
+      // would take one unit after another)
       uint4 codes[kUnits];
       uint32_t factor[kUnits];
 #pragma unroll
@@ -836,7 +837,9 @@ __device__ __noinline__ bool merge_copies(const CopyMerge& m, uint32_t phase) {
   return true;
 }
 constexpr uint32_t kMergeWaits = 5;
-constexpr int kMergeTiles = 16;  // of a whole group: fewer are not worth the merge, 11000 to 16000 cycles
+// Of a whole group: fewer are not worth the merge (12 nodes over 512 rows, 64
+// elements: 78 us with it, 56 without; e4m3 111 and 84).
+constexpr int kMergeTiles = 16;
 
 // A tile whose rows have their own scales: n columns of logits from `col` on become
 // z + e in log2 units (e of V), -inf where `vis` is not set.
@@ -919,8 +922,8 @@ __device__ __forceinline__ void tc_softmax(const TreeTcParams& P, unsigned char*
       }
       float f1 = 1.f, f2 = 1.f;
       if (C::F8) {
-        // as f16, scaled by a power of two to below 2 (exact for elements down to 2^-14
-        // of the row's largest, half of 2^-24 off below)
+        // as f16, scaled by a power of two to below 2 (exact for elements down to 2^-17
+        // of the row's largest: bf16's 8 bits end at f16's 2^-24; half of that off below)
         uint32_t mx = 0u;
         auto most = [&](const uint4& v) {
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};

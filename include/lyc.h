@@ -438,7 +438,11 @@ lyc_status lyc_sparse_attention_noalloc(const void* q, const lyc_kv_cache* kv, i
  * is exact in bf16 (within its range: magnitudes of 1.9375 * 2^127 and more
  * read back as infinite, and what is below its smallest number rounds).  A row that holds a NaN or
  * an infinity gets scale byte 255 and zero codes and reads back as NaN.
- * Codes 0x7f and 0xff (NaN) are never written and are not looked for. */
+ * Codes 0x7f and 0xff (NaN) are never written and are not looked for.
+ * The decode step (lyc_decode_step and its forms) reads bf16 or fp32 rows only,
+ * and pages of whole 64 rows: a layer of an E4M3 cache is read back before it
+ * (lyc_cache_read), which moves more bytes than the smaller cache saves.
+ * What reads E4M3 rows as they are is lyc_tree_attention. */
 typedef enum { LYC_CACHE_BF16 = 0, LYC_CACHE_E4M3 = 1 } lyc_cache_type;
 
 /* One layer's cache.  Row i of (element b, KV head g):
