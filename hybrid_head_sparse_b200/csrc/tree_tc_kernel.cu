@@ -31,27 +31,28 @@
 // e4m3 rows become f16 tiles on their way: code * 2^(e - E), E the largest e of the
 // tile's rows, so the products run in f16.  2^E of K is a factor of the tile's
 // logits; V's goes into the exponent, p' = 2^(z + E - m'), m' the running maximum of
-// z + E, and the sum takes p' 2^-E (kSumUnitE4m3).  That is exact while the tile's e are within 14
-// of each other, and V's are held within 6, so that p' of a row far below E does not
-// fall out of f16's range (at 14, a tail of 65536 rows 2^-18 below the top one was
-// lost beside a row of negligible probability 2^14 larger).  Where they are not (a row
-// of zeros; a drafted row that nobody has written or sees), the tile is the codes
-// alone and the softmax warps apply each row's scales.  A query row becomes f16 as in tree_mma_kernel.cu.  Three warps find
-// the rows of coming tiles and their scales; eight producer warps copy the codes
-// in, convert them (two instructions for two codes) and store them.
+// z + E, and the sum takes p' 2^-E (kSumUnitE4m3).  That is exact while the tile's e
+// are within 14 of each other, and V's are held within 6, so that p' of a row far
+// below E does not fall out of f16's range (at 14, a tail of 65536 rows 2^-18 below
+// the top one was lost beside a row of negligible probability 2^14 larger).  Where
+// they are not (a row of zeros; a drafted row that nobody has written or sees), the
+// tile is the codes alone and the softmax warps apply each row's scales.  A query row
+// becomes f16 as in tree_mma_kernel.cu.  Three warps find the rows of coming tiles
+// and their scales; eight producer warps copy the codes in, convert them (two
+// instructions for two codes) and store them.
 //
 // Device times, 32 query and 8 KV heads.  32 nodes over 131072 bf16 rows: 96 to
 // 101 us by the box, 5.3 to 5.6 TB/s, 0.81 to 0.85 of the copy rate: HBM, and the
 // exponentials (1024 cycles a tile at 16 a cycle).  4 x 16 nodes over up to 65536
 // e4m3 rows each: 165 us, 0.37 of the floor; 2 x 64 nodes over up to 32768 rows: 114 to 135.
 // There a tile's share is 2.0 us, its bytes' 0.75; counted, it needs 1000 cycles of
-// the tensor cores and 1800 of shared memory (128 bytes a cycle), and neither is busy
-// for more than a third of the time (half of the issue slots are): what bounds it is
-// the softmax warps' chain of latencies among twenty warps.  Slower were: bf16 tiles, codes converted by
-// bit moves (175); each row's own scale in the softmax, K's codes as an e4m3 operand
-// (212); codes brought by TMA (205); four or sixteen producers (190, 203); a fourth
-// finder (200: the schedulers' warps are no longer the same); one pass over the
-// logits (185).  Leaving out the check of the scales' spread gained 4.
+// the tensor cores and 1800 of shared memory (128 bytes a cycle), each of them less
+// than half of that, and the issue slots are half busy: what bounds it is the softmax
+// warps' chain of latencies among twenty warps.  Slower were: bf16 tiles, codes
+// converted by bit moves (175); each row's own scale in the softmax, K's codes as an
+// e4m3 operand (212); codes brought by TMA (205); four or sixteen producers (190,
+// 203); a fourth finder (200: the schedulers' warps are no longer the same); one pass
+// over the logits (185).  Leaving out the check of the scales' spread gained 4.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
